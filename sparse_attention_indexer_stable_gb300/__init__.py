@@ -1,14 +1,15 @@
 """GB300-native DCP sparse-indexer top-K: a thin Python binding of the C ABI.
 
 The compute lives in ``_build/libdcp_topk.so`` (CUDA, sm_103a), declared in
-``include/dcp_topk.h``.  This module only marshals torch tensors (device
+``include/dcp_topk.h`` and ``include/dcp_kv4.h``.  This module only marshals torch tensors (device
 memory) and the current CUDA stream into that ABI; every step of the top-K
 runs in the library's kernels.  There is no CPU fallback: if the library is
 missing or fails to load, every call raises.
 
 Functions with the ABI's names take raw device pointers and sizes, exactly like
 the C functions.  ``merge`` and ``local_topk`` are tensor conveniences on top
-of them that check shapes and dtypes and allocate outputs with torch.
+of them that check shapes and dtypes and allocate outputs with torch; the
+``kv4_*`` functions (module ``kv4``) are the same for the 4-bit key/value cache.
 """
 from __future__ import annotations
 
@@ -65,6 +66,7 @@ def library():
                 _build.build()
             lib = ctypes.CDLL(path)
             P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+            N = ctypes.c_int64
             lib.dcp_topk_merge.argtypes = [P, P, I, I, I, P, P, P, P, S, P]
             lib.dcp_topk_merge.restype = I
             lib.dcp_topk_merge_shards.argtypes = [P, P, I, I, I, P, P, P, P]
@@ -83,6 +85,16 @@ def library():
             lib.dcp_topk_device_status.restype = I
             lib.dcp_topk_selftest_wait_timeout.argtypes = [ctypes.c_uint, P]
             lib.dcp_topk_selftest_wait_timeout.restype = I
+            lib.dcp_kv4_append.argtypes = [P, P, P, I, N, N, N, N, N, P, P]
+            lib.dcp_kv4_append.restype = I
+            lib.dcp_kv4_read.argtypes = [P, P, P, I, N, P, P]
+            lib.dcp_kv4_read.restype = I
+            lib.dcp_kv4_attention_workspace_size.argtypes = [P, P, ctypes.POINTER(S)]
+            lib.dcp_kv4_attention_workspace_size.restype = I
+            lib.dcp_kv4_attention.argtypes = [P, P, P]
+            lib.dcp_kv4_attention.restype = I
+            lib.dcp_kv4_evict.argtypes = [P, P, P]
+            lib.dcp_kv4_evict.restype = I
             lib.dcp_status_string.argtypes = [I]
             lib.dcp_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -376,3 +388,9 @@ def fused_topk(logits, K, L=None, row_starts=None, out_scores=None, out_ids=None
     if st != DCP_OK:
         raise DcpError(st, "dcp_fused_topk_ex")
     return out_scores, out_ids
+
+
+from . import kv4 as _kv4  # noqa: E402  (uses the helpers above)
+from .kv4 import *  # noqa: E402,F401,F403
+
+__all__ += _kv4.__all__

@@ -1,6 +1,6 @@
 """Builds the CUDA library in-tree: csrc/*.cu -> _build/libdcp_topk.so (sm_103a).
 
-Plain nvcc, one translation unit, no CMake; host code has no
+Plain nvcc, one translation unit per subject compiled side by side, no CMake; host code has no
 architecture-specific flags so the same source builds on x86_64 and aarch64.
 """
 from __future__ import annotations
@@ -58,6 +58,7 @@ def build(force: bool = False, extra_flags=(), path: str = LIB_PATH) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     tmp = path + f".{os.getpid()}.tmp"
     cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--shared",
+           "--threads", "0",
            "-Xcompiler", "-fPIC", "-I", INCLUDE, "-o", tmp, *sources(), *extra_flags]
     subprocess.check_call(cmd)
     os.replace(tmp, path)

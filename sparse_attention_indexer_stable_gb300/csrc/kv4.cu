@@ -1,0 +1,348 @@
+// kv4.cu -- C ABI of the 4-bit key/value cache (include/dcp_kv4.h).
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include <atomic>
+#include <mutex>
+
+#include "dcp_kv4.h"
+#include "kv4_attention.cuh"
+#include "kv4_evict.cuh"
+#include "kv4_store.cuh"
+
+namespace dcp {
+namespace kv4 {
+
+static bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+static bool power_of_two(float f) {
+  uint32_t b;
+  static_assert(sizeof b == sizeof f, "");
+  __builtin_memcpy(&b, &f, sizeof b);
+  return (b & 0x807FFFFFu) == 0u && b != 0u && b != 0x7F800000u;
+}
+
+// Checks a cache and fills the kernels' view of it.
+static dcp_status planes_of(const dcp_kv4_cache* c, Planes* out) {
+  if (!c || c->num_pages < 0 || c->page_size < 1 || c->heads < 1 || c->dim < 1 ||
+      !power_of_two(c->k_unit) || !power_of_two(c->v_unit))
+    return DCP_ERR_INVALID;
+  if ((c->dim != 64 && c->dim != 128 && c->dim != 256) || c->page_size > 65536 ||
+      (c->page_size & (c->page_size - 1)) || c->heads > 65536)
+    return DCP_ERR_UNSUPPORTED;
+  int shift = 0;
+  while ((1 << shift) < c->page_size) ++shift;
+  if (c->num_pages >= (((int64_t)1 << 32) >> shift)) return DCP_ERR_UNSUPPORTED;
+  if (c->num_pages > 0 && (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales))
+    return DCP_ERR_INVALID;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 16) ||
+      !aligned(c->v_scales, 16))
+    return DCP_ERR_INVALID;
+  out->k_codes = c->k_codes;
+  out->v_codes = c->v_codes;
+  out->k_scales = c->k_scales;
+  out->v_scales = c->v_scales;
+  out->num_pages = (uint32_t)c->num_pages;
+  out->page_shift = shift;
+  out->heads = c->heads;
+  out->k_unit = c->k_unit;
+  out->v_unit = c->v_unit;
+  return DCP_OK;
+}
+
+static dcp_status status_of(cudaError_t e) { return e == cudaSuccess ? DCP_OK : DCP_ERR_CUDA; }
+
+// -------------------------------------------------------------- attention
+struct DeviceInfo {
+  int sms = 0;
+  std::atomic<bool> ready{false};
+};
+static DeviceInfo g_dev[64];
+static std::mutex g_dev_mutex;
+
+template <int D, int NT>
+static cudaError_t allow_smem() {
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<D, NT, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       AttentionShape<D, NT>::kSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attention_kernel<D, NT, true>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              AttentionShape<D, NT>::kSmem);
+}
+
+// Per-device kernel attributes, set once (the first call on a device must
+// therefore not be inside a stream capture).
+static cudaError_t device_info(DeviceInfo** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  DeviceInfo& d = g_dev[dev];
+  *out = &d;
+  if (d.ready.load(std::memory_order_acquire)) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(g_dev_mutex);
+  if (d.ready.load(std::memory_order_relaxed)) return cudaSuccess;
+  if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return e;
+  if ((e = allow_smem<64, 1>()) != cudaSuccess || (e = allow_smem<64, 2>()) != cudaSuccess ||
+      (e = allow_smem<128, 1>()) != cudaSuccess || (e = allow_smem<128, 2>()) != cudaSuccess ||
+      (e = allow_smem<256, 1>()) != cudaSuccess)
+    return e;
+  d.ready.store(true, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// How a call is cut up, and where its parts of the workspace lie.
+struct Plan {
+  int heads_per_cta, head_tiles, splits, limit, width;
+  size_t part_out, part_ml, scores, row_ml, bytes;
+};
+
+// The SM count that slices are sized for; the workspace's size may not depend
+// on a device being present.
+constexpr int kPlanSms = 152;
+// A slice holds at least this many tokens: one tile per warp.
+constexpr int kMinSlice = 16 * kAttWarps;
+
+static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
+                          const dcp_kv4_attention_args* a, Plan* plan) {
+  if (!a || (a->dtype != DCP_F16 && a->dtype != DCP_BF16) || a->rows < 0 || a->q_heads < 1 ||
+      a->q_heads % c->heads || a->num_seqs < 0 || a->table_width < 0 || a->max_len < 0 ||
+      (a->ids && a->num_ids < 0) || (a->weights && a->owner) || !(a->softcap >= 0.0f) ||
+      a->weights_width < 0)
+    return DCP_ERR_INVALID;
+  const int64_t capacity = (int64_t)a->table_width << planes.page_shift;
+  if (capacity > INT_MAX) return DCP_ERR_UNSUPPORTED;
+  plan->limit = (int)(a->max_len && a->max_len < capacity ? a->max_len : capacity);
+  plan->width = a->ids ? a->num_ids : plan->limit;
+  const int group = a->q_heads / c->heads;
+  plan->heads_per_cta = group > 8 && c->dim <= 128 ? 16 : 8;
+  plan->head_tiles = (group + plan->heads_per_cta - 1) / plan->heads_per_cta;
+  const int64_t units = (int64_t)a->rows * c->heads * plan->head_tiles;
+  int64_t splits = units > 0 ? (2 * kPlanSms + units - 1) / units : 1;
+  const int64_t most = plan->width / kMinSlice;
+  if (splits > most) splits = most;
+  if (splits < 1) splits = 1;
+  if (units * splits > INT_MAX || (int64_t)a->rows * a->q_heads > INT_MAX)
+    return DCP_ERR_UNSUPPORTED;
+  plan->splits = (int)splits;
+  const size_t heads = (size_t)a->rows * a->q_heads;
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 15) & ~(size_t)15;
+    return here;
+  };
+  plan->part_out = plan->part_ml = plan->scores = plan->row_ml = 0;
+  if (splits > 1) {
+    plan->part_out = take(heads * splits * c->dim * sizeof(float));
+    plan->part_ml = take(heads * splits * sizeof(float2));
+  }
+  if (a->weights) {
+    plan->scores = take(heads * plan->width * sizeof(float));
+    plan->row_ml = take(heads * sizeof(float2));
+  }
+  plan->bytes = at;
+  return DCP_OK;
+}
+
+template <int D, int NT>
+static cudaError_t launch_attention(const AttentionParams& p, cudaStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.head_tiles * p.c.heads));
+  cudaError_t e =
+      launch(p.ids ? attention_kernel<D, NT, true> : attention_kernel<D, NT, false>, grid,
+             kAttThreads, AttentionShape<D, NT>::kSmem, 1, stream, p);
+  if (e != cudaSuccess) return e;
+  if (p.splits > 1)
+    e = launch(join_kernel<D>, dim3((unsigned)((int64_t)p.rows * p.q_heads)), 128, 0, 1, stream, p);
+  return e;
+}
+
+static cudaError_t launch_all(const AttentionParams& p, int dim, int heads_per_cta,
+                              cudaStream_t stream) {
+  cudaError_t e;
+  if (dim == 64)
+    e = heads_per_cta == 16 ? launch_attention<64, 2>(p, stream)
+                            : launch_attention<64, 1>(p, stream);
+  else if (dim == 128)
+    e = heads_per_cta == 16 ? launch_attention<128, 2>(p, stream)
+                            : launch_attention<128, 1>(p, stream);
+  else
+    e = launch_attention<256, 1>(p, stream);
+  if (e != cudaSuccess || !p.weights || p.width == 0) return e;
+  const int64_t tiles = ((int64_t)p.width + kWeightTokens - 1) / kWeightTokens;
+  return launch(p.ids ? weights_kernel<true> : weights_kernel<false>,
+                dim3((unsigned)(p.rows * tiles)), 256, (size_t)p.q_heads * sizeof(float2), 1,
+                stream, p);
+}
+
+}  // namespace kv4
+}  // namespace dcp
+
+using namespace dcp::kv4;
+
+extern "C" {
+
+static dcp_status store_args(const dcp_kv4_cache* cache, const void* k, const void* v, int dtype,
+                             int64_t N, const int64_t* slots, StoreParams* p) {
+  const dcp_status st = planes_of(cache, &p->c);
+  if (st != DCP_OK) return st;
+  if (dtype != DCP_F16 && dtype != DCP_BF16 && dtype != DCP_F32) return DCP_ERR_INVALID;
+  if (N < 0) return DCP_ERR_INVALID;
+  p->blocks = cache->dim / kBlock;
+  p->N = N;
+  p->dtype = dtype;
+  p->slots = slots;
+  if (N == 0) return DCP_OK;
+  if (!k || !v || !slots) return DCP_ERR_INVALID;
+  if (N > (int64_t)INT_MAX * 256 / ((int64_t)cache->heads * p->blocks)) return DCP_ERR_UNSUPPORTED;
+  return DCP_OK;
+}
+
+static dim3 store_grid(const StoreParams& p) {
+  return dim3((unsigned)((p.N * p.c.heads * p.blocks + 255) / 256), 2);
+}
+
+dcp_status dcp_kv4_append(const dcp_kv4_cache* cache, const void* k, const void* v, int dtype,
+                          int64_t N, int64_t k_row_stride, int64_t k_head_stride,
+                          int64_t v_row_stride, int64_t v_head_stride, const int64_t* slots,
+                          dcp_stream_t stream) {
+  StoreParams p{};
+  const dcp_status st = store_args(cache, k, v, dtype, N, slots, &p);
+  if (st != DCP_OK || N == 0) return st;
+  p.in[0] = k, p.in[1] = v;
+  p.row_stride[0] = k_row_stride, p.row_stride[1] = v_row_stride;
+  p.head_stride[0] = k_head_stride, p.head_stride[1] = v_head_stride;
+  const int64_t per = dtype == DCP_F32 ? 4 : 8;  // elements in 16 bytes
+  for (int i = 0; i < 2; ++i)
+    p.vec[i] = aligned(p.in[i], 16) && p.row_stride[i] % per == 0 && p.head_stride[i] % per == 0;
+  return status_of(launch(append_kernel, store_grid(p), 256, 0, 1, (cudaStream_t)stream, p));
+}
+
+dcp_status dcp_kv4_read(const dcp_kv4_cache* cache, void* k, void* v, int dtype, int64_t N,
+                        const int64_t* slots, dcp_stream_t stream) {
+  StoreParams p{};
+  const dcp_status st = store_args(cache, k, v, dtype, N, slots, &p);
+  if (st != DCP_OK || N == 0) return st;
+  if (!aligned(k, 16) || !aligned(v, 16)) return DCP_ERR_INVALID;
+  p.out[0] = k, p.out[1] = v;
+  return status_of(launch(read_kernel, store_grid(p), 256, 0, 1, (cudaStream_t)stream, p));
+}
+
+dcp_status dcp_kv4_attention_workspace_size(const dcp_kv4_cache* cache,
+                                            const dcp_kv4_attention_args* args, size_t* bytes) {
+  Planes planes;
+  Plan plan;
+  if (!bytes) return DCP_ERR_INVALID;
+  dcp_status st = planes_of(cache, &planes);
+  if (st == DCP_OK) st = plan_of(cache, planes, args, &plan);
+  if (st == DCP_OK) *bytes = plan.bytes;
+  return st;
+}
+
+dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention_args* a,
+                             dcp_stream_t stream) {
+  AttentionParams p{};
+  Plan plan;
+  dcp_status st = planes_of(cache, &p.c);
+  if (st == DCP_OK) st = plan_of(cache, p.c, a, &plan);
+  if (st != DCP_OK || a->rows == 0) return st;
+  if (!a->q || !a->lens || !a->out || !a->lse || (!a->table && plan.limit > 0) ||
+      (a->owner == nullptr && a->num_seqs < a->rows))
+    return DCP_ERR_INVALID;
+  if (!aligned(a->out, 16) || !aligned(a->workspace, 16)) return DCP_ERR_INVALID;
+  if (plan.bytes > 0 && (!a->workspace || a->workspace_bytes < plan.bytes)) return DCP_ERR_INVALID;
+  p.q = a->q;
+  p.q_row_stride = a->q_row_stride;
+  p.q_head_stride = a->q_head_stride;
+  p.q_vec = aligned(a->q, 16) && a->q_row_stride % 8 == 0 && a->q_head_stride % 8 == 0;
+  p.table = a->table;
+  p.table_stride = a->table_stride;
+  p.lens = a->lens;
+  p.starts = a->starts;
+  p.owner = a->owner;
+  p.ids = a->ids;
+  p.ids_stride = a->ids_stride;
+  p.num_ids = a->num_ids;
+  p.row_starts = a->row_starts;
+  p.out = a->out;
+  p.lse = a->lse;
+  unsigned char* ws = static_cast<unsigned char*>(a->workspace);
+  if (plan.splits > 1) {
+    p.part_out = reinterpret_cast<float*>(ws + plan.part_out);
+    p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  }
+  if (a->weights) {
+    p.scores = reinterpret_cast<float*>(ws + plan.scores);
+    p.row_ml = reinterpret_cast<float2*>(ws + plan.row_ml);
+  }
+  p.weights = a->weights;
+  p.weights_stride = a->weights_stride;
+  p.weights_width = a->weights_width;
+  p.dtype = a->dtype;
+  p.rows = a->rows;
+  p.q_heads = a->q_heads;
+  p.group = a->q_heads / cache->heads;
+  p.head_tiles = plan.head_tiles;
+  p.num_seqs = a->num_seqs;
+  p.splits = plan.splits;
+  p.limit = plan.limit;
+  p.width = plan.width;
+  p.scale = (a->scale != 0.0f ? a->scale : 1.0f / sqrtf((float)cache->dim)) * cache->k_unit;
+  p.softcap = a->softcap;
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != cudaSuccess) return DCP_ERR_CUDA;
+  return status_of(launch_all(p, cache->dim, plan.heads_per_cta, (cudaStream_t)stream));
+}
+
+dcp_status dcp_kv4_evict(const dcp_kv4_cache* cache, const dcp_kv4_evict_args* a,
+                         dcp_stream_t stream) {
+  EvictParams p{};
+  const dcp_status st = planes_of(cache, &p.c);
+  if (st != DCP_OK) return st;
+  if (!a || a->num_seqs < 0 || a->table_width < 0 || a->weights_width < 0 || a->budget < 1 ||
+      a->sinks < 0 || a->recent < 0 || (int64_t)a->sinks + a->recent > a->budget)
+    return DCP_ERR_INVALID;
+  const int64_t capacity = (int64_t)a->table_width << p.c.page_shift;
+  const int64_t limit = capacity < a->weights_width ? capacity : a->weights_width;
+  if (capacity > INT_MAX || (int64_t)a->num_seqs * a->budget > (int64_t)INT_MAX * 8 ||
+      a->num_seqs > INT_MAX / 8)
+    return DCP_ERR_UNSUPPORTED;
+  if (a->num_seqs == 0) return DCP_OK;
+  if (!a->lens || !a->out_table || !a->kept || !a->out_lens || !a->out_weights ||
+      (limit > 0 && (!a->table || !a->weights)))
+    return DCP_ERR_INVALID;
+  p.table = a->table;
+  p.table_stride = a->table_stride;
+  p.lens = a->lens;
+  p.weights = a->weights;
+  p.weights_stride = a->weights_stride;
+  p.out_table = a->out_table;
+  p.out_table_stride = a->out_table_stride;
+  p.kept = a->kept;
+  p.out_lens = a->out_lens;
+  p.out_weights = a->out_weights;
+  p.num_seqs = a->num_seqs;
+  p.limit = (int)limit;
+  p.budget = a->budget;
+  p.sinks = a->sinks;
+  p.recent = a->recent;
+  p.row_codes = cache->heads * cache->dim / 2;
+  p.row_scales = cache->heads * cache->dim / kBlock;
+  // CTAs per sequence: 8192 weights each, up to a portable cluster
+  int ctas = 1;
+  while (ctas < 8 && (int64_t)ctas * 8192 < limit) ctas *= 2;
+  cudaError_t e = launch(evict_select_kernel, dim3((unsigned)(a->num_seqs * ctas)), kSelThreads, 0,
+                         ctas, (cudaStream_t)stream, p);
+  if (e != cudaSuccess) return DCP_ERR_CUDA;
+  const int64_t items = (int64_t)a->num_seqs * a->budget;
+  e = launch(evict_copy_kernel, dim3((unsigned)((items + 7) / 8)), 256, 0, 1, (cudaStream_t)stream,
+             p);
+  return status_of(e);
+}
+
+}  // extern "C"

@@ -56,57 +56,62 @@ static dcp_status planes_of(const dcp_kv4_cache* c, Planes* out) {
 static dcp_status status_of(cudaError_t e) { return e == cudaSuccess ? DCP_OK : DCP_ERR_CUDA; }
 
 // -------------------------------------------------------------- attention
-struct DeviceInfo {
-  int sms = 0;
-  std::atomic<bool> ready{false};
-};
-static DeviceInfo g_dev[64];
+static std::atomic<bool> g_ready[64];
 static std::mutex g_dev_mutex;
 
+template <typename Kernel>
+static cudaError_t allow_smem(Kernel* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <int D, int NT>
-static cudaError_t allow_smem() {
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<D, NT, false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       AttentionShape<D, NT>::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attention_kernel<D, NT, true>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              AttentionShape<D, NT>::kSmem);
+static cudaError_t allow_attention() {
+  constexpr int kBytes = AttentionShape<D, NT>::kSmem;
+  cudaError_t e;
+  if ((e = allow_smem(attention_slices_kernel<D, NT, false>, kBytes)) != cudaSuccess ||
+      (e = allow_smem(attention_slices_kernel<D, NT, true>, kBytes)) != cudaSuccess ||
+      (e = allow_smem(attention_shares_kernel<D, NT, false>, kBytes)) != cudaSuccess)
+    return e;
+  return allow_smem(attention_shares_kernel<D, NT, true>, kBytes);
 }
 
 // Per-device kernel attributes, set once (the first call on a device must
 // therefore not be inside a stream capture).
-static cudaError_t device_info(DeviceInfo** out) {
+static cudaError_t prepare_device() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  DeviceInfo& d = g_dev[dev];
-  *out = &d;
-  if (d.ready.load(std::memory_order_acquire)) return cudaSuccess;
+  if (g_ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
   std::lock_guard<std::mutex> lock(g_dev_mutex);
-  if (d.ready.load(std::memory_order_relaxed)) return cudaSuccess;
-  if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+  if ((e = allow_attention<64, 1>()) != cudaSuccess ||
+      (e = allow_attention<64, 2>()) != cudaSuccess ||
+      (e = allow_attention<128, 1>()) != cudaSuccess ||
+      (e = allow_attention<128, 2>()) != cudaSuccess ||
+      (e = allow_attention<256, 1>()) != cudaSuccess)
     return e;
-  if ((e = allow_smem<64, 1>()) != cudaSuccess || (e = allow_smem<64, 2>()) != cudaSuccess ||
-      (e = allow_smem<128, 1>()) != cudaSuccess || (e = allow_smem<128, 2>()) != cudaSuccess ||
-      (e = allow_smem<256, 1>()) != cudaSuccess)
-    return e;
-  d.ready.store(true, std::memory_order_release);
+  g_ready[dev].store(true, std::memory_order_release);
   return cudaSuccess;
 }
 
-// How a call is cut up, and where its parts of the workspace lie.
+// How a call is cut up (see kv4_attention.cuh), and where its parts of the
+// workspace lie.
 struct Plan {
-  int heads_per_cta, head_tiles, splits, limit, width;
-  size_t part_out, part_ml, scores, row_ml, bytes;
+  int heads_per_cta, head_tiles, limit, width;
+  int slices;  // CTAs of a row and head, when > 0
+  int shares;  // even shares, when > 0
+  int together;  // key/value heads that a share walks at the same time
+  size_t records, part_out, part_ml, scores, row_mult, row_ml, bytes;
 };
 
-// The SM count that slices are sized for; the workspace's size may not depend
+// The SM count that a call is cut up for: the workspace's size may not depend
 // on a device being present.
 constexpr int kPlanSms = 152;
-// A slice holds at least this many tokens: one tile per warp.
-constexpr int kMinSlice = 16 * kAttWarps;
+// What even shares cost beyond their tiles, in tiles of a warp: finding the
+// share's row, and the second launch.
+constexpr int64_t kShareCost = 3;
+// And what a piece costs: its queries, filling the ring, the join of its warps.
+constexpr int64_t kPieceCost = 2;
 
 static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
                           const dcp_kv4_attention_args* a, Plan* plan) {
@@ -122,14 +127,30 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   const int group = a->q_heads / c->heads;
   plan->heads_per_cta = group > 8 && c->dim <= 128 ? 16 : 8;
   plan->head_tiles = (group + plan->heads_per_cta - 1) / plan->heads_per_cta;
+  // Slices or shares, whichever has fewer tiles on its longest warp.  Lengths
+  // are on the device: both are judged at the longest row.
   const int64_t units = (int64_t)a->rows * c->heads * plan->head_tiles;
-  int64_t splits = units > 0 ? (2 * kPlanSms + units - 1) / units : 1;
-  const int64_t most = plan->width / kMinSlice;
-  if (splits > most) splits = most;
-  if (splits < 1) splits = 1;
-  if (units * splits > INT_MAX || (int64_t)a->rows * a->q_heads > INT_MAX)
-    return DCP_ERR_UNSUPPORTED;
-  plan->splits = (int)splits;
+  const int64_t tiles = ((int64_t)plan->width + kTile - 1) / kTile;
+  const bool wide = c->dim * plan->heads_per_cta >= 2048;  // one CTA per SM
+  const int64_t slots = kPlanSms * (wide ? 1 : 2);
+  auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  int64_t least = INT64_MAX;
+  plan->shares = 0;
+  for (int s = 1; s <= 8; s *= 2) {
+    const int64_t steps = ceil_div(units * s, slots) *
+                          (ceil_div(ceil_div(tiles, s), kAttWarps) + kPieceCost);
+    if (steps < least) least = steps, plan->slices = s;
+  }
+  // the largest power of two that leaves at most a fifth of the warps idle
+  plan->together = kAttWarps;
+  while (ceil_div(c->heads, plan->together) * plan->together * 4 > c->heads * 5)
+    plan->together /= 2;
+  const int64_t padded = units / c->heads * ceil_div(c->heads, plan->together) * plan->together;
+  if (ceil_div(padded * tiles, slots * kAttWarps) + kPieceCost + kShareCost < least) {
+    plan->slices = 0;
+    plan->shares = (int)slots;
+  }
+  if (units * 8 > INT_MAX || (int64_t)a->rows * a->q_heads > INT_MAX) return DCP_ERR_UNSUPPORTED;
   const size_t heads = (size_t)a->rows * a->q_heads;
   size_t at = 0;
   auto take = [&at](size_t bytes) {
@@ -137,13 +158,17 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
     at += (bytes + 15) & ~(size_t)15;
     return here;
   };
-  plan->part_out = plan->part_ml = plan->scores = plan->row_ml = 0;
-  if (splits > 1) {
-    plan->part_out = take(heads * splits * c->dim * sizeof(float));
-    plan->part_ml = take(heads * splits * sizeof(float2));
+  plan->records = plan->part_out = plan->part_ml = plan->scores = 0;
+  plan->row_mult = plan->row_ml = 0;
+  if (plan->shares) {
+    const size_t pieces = (size_t)plan->shares * 2 * plan->together * plan->heads_per_cta;
+    plan->records = take(plan->shares * sizeof(int4));
+    plan->part_out = take(pieces * c->dim * sizeof(float));
+    plan->part_ml = take(pieces * sizeof(float2));
   }
   if (a->weights) {
     plan->scores = take(heads * plan->width * sizeof(float));
+    plan->row_mult = take(heads * sizeof(float));
     plan->row_ml = take(heads * sizeof(float2));
   }
   plan->bytes = at;
@@ -151,32 +176,47 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
 }
 
 template <int D, int NT>
-static cudaError_t launch_attention(const AttentionParams& p, cudaStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.head_tiles * p.c.heads));
-  cudaError_t e =
-      launch(p.ids ? attention_kernel<D, NT, true> : attention_kernel<D, NT, false>, grid,
-             kAttThreads, AttentionShape<D, NT>::kSmem, 1, stream, p);
+static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
+                                    cudaStream_t stream) {
+  constexpr int kBytes = AttentionShape<D, NT>::kSmem;
+  if (plan.slices) {
+    const unsigned grid = (unsigned)p.rows * p.head_tiles * p.c.heads * plan.slices;
+    return launch(p.ids ? attention_slices_kernel<D, NT, true>
+                        : attention_slices_kernel<D, NT, false>,
+                  dim3(grid), kAttThreads, kBytes, plan.slices, stream, p);
+  }
+  const cudaError_t e = launch(p.ids ? attention_shares_kernel<D, NT, true>
+                                     : attention_shares_kernel<D, NT, false>,
+                               dim3((unsigned)plan.shares), kAttThreads, kBytes, 1, stream, p);
   if (e != cudaSuccess) return e;
-  if (p.splits > 1)
-    e = launch(join_kernel<D>, dim3((unsigned)((int64_t)p.rows * p.q_heads)), 128, 0, 1, stream, p);
-  return e;
+  const int units = (p.c.heads + p.together - 1) / p.together * p.head_tiles;
+  const int heads = p.together * 8 * NT;
+  // a unit is cut into about shares / (rows * units) pieces: from 16 on, two
+  // for each warp of a CTA, a CTA joins one head, otherwise a warp does
+  if ((int64_t)p.rows * units * 16 <= plan.shares)
+    return launch(join_shares_kernel<D, NT, true>,
+                  dim3((unsigned)(p.rows * units), (unsigned)heads), 32 * kJoinWarps, 0, 1, stream,
+                  p, plan.shares);
+  return launch(join_shares_kernel<D, NT, false>,
+                dim3((unsigned)plan.shares, (unsigned)(heads / kJoinWarps)), 32 * kJoinWarps, 0, 1,
+                stream, p, plan.shares);
 }
 
-static cudaError_t launch_all(const AttentionParams& p, int dim, int heads_per_cta,
+static cudaError_t launch_all(const AttentionParams& p, int dim, const Plan& plan,
                               cudaStream_t stream) {
   cudaError_t e;
   if (dim == 64)
-    e = heads_per_cta == 16 ? launch_attention<64, 2>(p, stream)
-                            : launch_attention<64, 1>(p, stream);
+    e = plan.heads_per_cta == 16 ? launch_attention<64, 2>(p, plan, stream)
+                                 : launch_attention<64, 1>(p, plan, stream);
   else if (dim == 128)
-    e = heads_per_cta == 16 ? launch_attention<128, 2>(p, stream)
-                            : launch_attention<128, 1>(p, stream);
+    e = plan.heads_per_cta == 16 ? launch_attention<128, 2>(p, plan, stream)
+                                 : launch_attention<128, 1>(p, plan, stream);
   else
-    e = launch_attention<256, 1>(p, stream);
+    e = launch_attention<256, 1>(p, plan, stream);
   if (e != cudaSuccess || !p.weights || p.width == 0) return e;
   const int64_t tiles = ((int64_t)p.width + kWeightTokens - 1) / kWeightTokens;
   return launch(p.ids ? weights_kernel<true> : weights_kernel<false>,
-                dim3((unsigned)(p.rows * tiles)), 256, (size_t)p.q_heads * sizeof(float2), 1,
+                dim3((unsigned)(p.rows * tiles)), 256, (size_t)p.q_heads * 3 * sizeof(float), 1,
                 stream, p);
 }
 
@@ -272,12 +312,14 @@ dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention
   p.out = a->out;
   p.lse = a->lse;
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
-  if (plan.splits > 1) {
+  if (plan.shares) {
+    p.shares = reinterpret_cast<int4*>(ws + plan.records);
     p.part_out = reinterpret_cast<float*>(ws + plan.part_out);
     p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
   }
   if (a->weights) {
     p.scores = reinterpret_cast<float*>(ws + plan.scores);
+    p.row_mult = reinterpret_cast<float*>(ws + plan.row_mult);
     p.row_ml = reinterpret_cast<float2*>(ws + plan.row_ml);
   }
   p.weights = a->weights;
@@ -288,15 +330,15 @@ dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention
   p.q_heads = a->q_heads;
   p.group = a->q_heads / cache->heads;
   p.head_tiles = plan.head_tiles;
+  p.together = plan.together;
   p.num_seqs = a->num_seqs;
-  p.splits = plan.splits;
   p.limit = plan.limit;
   p.width = plan.width;
+  p.score_pairs = a->q_heads % 2 == 0 && p.group % 2 == 0;
   p.scale = (a->scale != 0.0f ? a->scale : 1.0f / sqrtf((float)cache->dim)) * cache->k_unit;
   p.softcap = a->softcap;
-  DeviceInfo* d = nullptr;
-  if (device_info(&d) != cudaSuccess) return DCP_ERR_CUDA;
-  return status_of(launch_all(p, cache->dim, plan.heads_per_cta, (cudaStream_t)stream));
+  if (prepare_device() != cudaSuccess) return DCP_ERR_CUDA;
+  return status_of(launch_all(p, cache->dim, plan, (cudaStream_t)stream));
 }
 
 dcp_status dcp_kv4_evict(const dcp_kv4_cache* cache, const dcp_kv4_evict_args* a,

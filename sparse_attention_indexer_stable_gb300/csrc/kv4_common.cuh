@@ -58,6 +58,26 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// a times the low, or the high, half of s.
+__device__ __forceinline__ uint32_t hmul2_low(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2_rn(*reinterpret_cast<const __half2*>(&a),
+                               __low2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmul2_high(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2_rn(*reinterpret_cast<const __half2*>(&a),
+                               __high2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// base + row * stride, in one wide multiply-add.
+__device__ __forceinline__ const uint8_t* row_at(const uint8_t* base, uint32_t row,
+                                                 uint32_t stride) {
+  const uint8_t* r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(row), "r"(stride), "l"(base));
+  return r;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -75,6 +95,16 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool ok)
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
                  "r"(n)
+                 : "memory");
+}
+
+// The same without the choice.
+template <int N>
+__device__ __forceinline__ void cp_async_all(uint32_t dst, const void* src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N)
                  : "memory");
 }
 

@@ -188,21 +188,43 @@ def test_dense_attention_at_edge_lengths(dk, dtype, dim, heads, group, page):
     check(dk, cache, host, q, values, dtype, table, np.array(EDGES))
 
 
-@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("width", [80, 1200])
+@pytest.mark.parametrize("dim,group", [(64, 2), (128, 2), (256, 2), (64, 20), (128, 17), (256, 9)])
 @pytest.mark.parametrize("lens", [[5000], [1, 4999, 777], [0, 0]])
-def test_few_long_rows_are_split_and_joined(dk, dim, lens):
+def test_few_long_rows_are_split_and_joined(dk, dim, group, lens, width):
+    """Cut into slices of a cluster (the narrow table) or into even shares
+    (the wide one, as if rows could be long), the pieces joined."""
     rng = np.random.default_rng(sum(lens) + dim)
     cache, host = fill(dk, rng, 100, 64, 1, dim)
-    table = table_of(rng, len(lens), 80, 100)
-    q, values = query(rng, len(lens), 2, dim, "bf16")
-    need = dk.kv4_attention_workspace_size(cache, len(lens), 2, 80)
-    assert need > 0  # split
+    table = table_of(rng, len(lens), width, 100)
+    q, values = query(rng, len(lens), group, dim, "bf16")
+    need = dk.kv4_attention_workspace_size(cache, len(lens), group, width)
+    assert (need > 0) == (width == 1200)  # only shares need a workspace
     out, lse = check(dk, cache, host, q, values, "bf16", table, np.array(lens))
     again = dk.kv4_attention(cache, q, i32(table), i32(lens))
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
     # a bound of the lengths changes the split, and cuts longer rows
     check(dk, cache, host, q, values, "bf16", table, np.array(lens), max_len=max(1, max(lens)))
     check(dk, cache, host, q, values, "bf16", table, np.array(lens), max_len=300)
+
+
+def test_even_shares_over_many_rows_of_all_lengths(dk):
+    """Shares that begin and end inside rows, rows of no tokens between them,
+    several heads and head tiles, for a range and for ids."""
+    rng = np.random.default_rng(22)
+    cache, host = fill(dk, rng, 60, 64, 2, 64)
+    rows = 310
+    lens = rng.integers(0, 700, rows)
+    lens[rng.random(rows) < 0.3] = 0
+    lens[[0, 1, 150, 309]] = [0, 3000, 3840, 0]
+    table = table_of(rng, rows, 300, 60)
+    q, values = query(rng, rows, 2 * 18, 64, "f16")
+    assert dk.kv4_attention_workspace_size(cache, rows, 36, 300) > 0
+    check(dk, cache, host, q, values, "f16", table, lens)
+    few = slice(145, 155)
+    ids = rng.permuted(np.tile(np.arange(19200), (10, 1)), axis=1)
+    assert dk.kv4_attention_workspace_size(cache, 10, 36, 300, num_ids=19200) > 0
+    check(dk, cache, host, q[few], values[few], "f16", table[few], lens[few], ids=ids)
 
 
 def test_starts_negative_lengths_and_lengths_beyond_the_table(dk):
@@ -381,9 +403,9 @@ def test_attention_on_another_stream_and_in_a_graph(dk):
 def test_given_outputs_and_workspace_are_used(dk):
     rng = np.random.default_rng(19)
     cache, host = fill(dk, rng, 100, 64, 1, 64)
-    table = i32(table_of(rng, 1, 100, 100))
+    table = i32(table_of(rng, 1, 1000, 100))
     q, _ = query(rng, 1, 4, 64, "f16")
-    need = dk.kv4_attention_workspace_size(cache, 1, 4, 100)
+    need = dk.kv4_attention_workspace_size(cache, 1, 4, 1000)
     space = torch.empty(need, dtype=torch.uint8, device=DEV)
     out = torch.empty(1, 4, 64, dtype=torch.float16, device=DEV)
     lse = torch.empty(1, 4, device=DEV)

@@ -11,6 +11,8 @@
 #include "dcp_kv4.h"
 #include "kv4_attention.cuh"
 #include "kv4_evict.cuh"
+#include "kv4_shares.cuh"
+#include "kv4_slices.cuh"
 #include "kv4_store.cuh"
 
 namespace dcp {
@@ -66,7 +68,7 @@ static cudaError_t allow_smem(Kernel* kernel, int bytes) {
 
 template <int D, int NT>
 static cudaError_t allow_attention() {
-  constexpr int kBytes = AttentionShape<D, NT>::kSmem;
+  constexpr int kBytes = RingShape<D, NT>::kSmem;
   cudaError_t e;
   if ((e = allow_smem(attention_slices_kernel<D, NT, false>, kBytes)) != cudaSuccess ||
       (e = allow_smem(attention_slices_kernel<D, NT, true>, kBytes)) != cudaSuccess ||
@@ -94,7 +96,7 @@ static cudaError_t prepare_device() {
   return cudaSuccess;
 }
 
-// How a call is cut up (see kv4_attention.cuh), and where its parts of the
+// How a call is cut up (see kv4_slices.cuh, kv4_shares.cuh), and where its parts of the
 // workspace lie.
 struct Plan {
   int heads_per_cta, head_tiles, limit, width;
@@ -135,22 +137,22 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   const int64_t slots = kPlanSms * (wide ? 1 : 2);
   auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   int64_t least = INT64_MAX;
-  plan->shares = 0;
   for (int s = 1; s <= 8; s *= 2) {
     const int64_t steps = ceil_div(units * s, slots) *
-                          (ceil_div(ceil_div(tiles, s), kAttWarps) + kPieceCost);
+                          (ceil_div(ceil_div(tiles, s), kWarps) + kPieceCost);
     if (steps < least) least = steps, plan->slices = s;
   }
   // the largest power of two that leaves at most a fifth of the warps idle
-  plan->together = kAttWarps;
+  plan->together = kWarps;
   while (ceil_div(c->heads, plan->together) * plan->together * 4 > c->heads * 5)
     plan->together /= 2;
   const int64_t padded = units / c->heads * ceil_div(c->heads, plan->together) * plan->together;
-  if (ceil_div(padded * tiles, slots * kAttWarps) + kPieceCost + kShareCost < least) {
+  plan->shares = 0;
+  if (ceil_div(padded * tiles, slots * kWarps) + kPieceCost + kShareCost < least) {
     plan->slices = 0;
     plan->shares = (int)slots;
   }
-  if (units * 8 > INT_MAX || (int64_t)a->rows * a->q_heads > INT_MAX) return DCP_ERR_UNSUPPORTED;
+  if (units * 8 > INT_MAX || units * (tiles + 1) / kPlanSms > INT_MAX || (int64_t)a->rows * a->q_heads > INT_MAX) return DCP_ERR_UNSUPPORTED;
   const size_t heads = (size_t)a->rows * a->q_heads;
   size_t at = 0;
   auto take = [&at](size_t bytes) {
@@ -178,16 +180,16 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
 template <int D, int NT>
 static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
                                     cudaStream_t stream) {
-  constexpr int kBytes = AttentionShape<D, NT>::kSmem;
+  constexpr int kBytes = RingShape<D, NT>::kSmem;
   if (plan.slices) {
     const unsigned grid = (unsigned)p.rows * p.head_tiles * p.c.heads * plan.slices;
     return launch(p.ids ? attention_slices_kernel<D, NT, true>
                         : attention_slices_kernel<D, NT, false>,
-                  dim3(grid), kAttThreads, kBytes, plan.slices, stream, p);
+                  dim3(grid), kThreads, kBytes, plan.slices, stream, p);
   }
   const cudaError_t e = launch(p.ids ? attention_shares_kernel<D, NT, true>
                                      : attention_shares_kernel<D, NT, false>,
-                               dim3((unsigned)plan.shares), kAttThreads, kBytes, 1, stream, p);
+                               dim3((unsigned)plan.shares), kThreads, kBytes, 1, stream, p);
   if (e != cudaSuccess) return e;
   const int units = (p.c.heads + p.together - 1) / p.together * p.head_tiles;
   const int heads = p.together * 8 * NT;

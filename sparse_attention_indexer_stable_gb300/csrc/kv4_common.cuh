@@ -31,8 +31,11 @@ struct Planes {
   __device__ uint64_t num_slots() const { return (uint64_t)num_pages << page_shift; }
 };
 
+// Waits until the stream's previous kernel is complete and visible, then lets
+// the next one be scheduled (it waits here in its turn).
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Four bytes of two codes each -> four fp16 pairs, the low nibble in the low

@@ -1,0 +1,137 @@
+// kv4_slices.cuh -- attention of short rows: a cluster of 1, 2, 4 or 8 CTAs per
+// row and key/value head, each a slice of the row's tiles dealt to its 8 warps,
+// joined through distributed shared memory.  One launch, no workspace.  Bound
+// by latency: a row of 2048 tokens is one tile per warp and slice.
+#pragma once
+
+#include "kv4_ring.cuh"
+
+namespace dcp {
+namespace kv4 {
+
+// The join, in the ring's place: each warp's outputs (padded rows), references
+// and sums, and behind them the CTA's own for the cluster (16 bytes per output
+// pair).
+template <int D, int NT>
+struct SliceJoin {
+  static constexpr int kStride = D + 4;
+  static constexpr int kWarpBytes = (kWarps * 8 * NT * (kStride + 2) * 4 + 15) & ~15;
+  static_assert(kWarpBytes + 8 * NT * D / 2 * 16 <= RingShape<D, NT>::kSmem, "fits the ring");
+};
+
+// Leaves a warp's sums in shared memory (all warps of the CTA: barriers).
+template <int D, int NT>
+__device__ __forceinline__ void leave_sums(const Heads<D, NT>& hd, uint8_t* smem) {
+  using Join = SliceJoin<D, NT>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, tq = lane & 3;
+  __syncthreads();  // every warp has read its ring
+  float* join_o = reinterpret_cast<float*>(smem);
+  float* join_m = join_o + kWarps * 8 * NT * Join::kStride;
+  float* join_l = join_m + kWarps * 8 * NT;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float sum = hd.l[n][c];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const int col = warp * 8 * NT + 8 * n + 2 * tq + c;
+      if (g == 0) join_m[col] = hd.m[n][c], join_l[col] = sum;
+      float* dst = join_o + col * Join::kStride + g * (D / 8);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(hd.o[n][i][c], hd.o[n][i][c + 2]);
+    }
+  __syncthreads();
+}
+
+// What leave_sums left, added over the warps: reference, sum and two outputs
+// of `head` at element d.
+template <int D, int NT>
+__device__ __forceinline__ Joined join_warps(const uint8_t* smem, int head, int d) {
+  using Join = SliceJoin<D, NT>;
+  const float* join_o = reinterpret_cast<const float*>(smem);
+  const float* join_m = join_o + kWarps * 8 * NT * Join::kStride;
+  const float* join_l = join_m + kWarps * 8 * NT;
+  Joined j{kNoScore, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) j.top = fmaxf(j.top, join_m[w * 8 * NT + head]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int col = w * 8 * NT + head;
+    const float f = exp2_approx(join_m[col] - j.top);
+    const float2 v = *reinterpret_cast<const float2*>(join_o + col * Join::kStride + d);
+    j.sum += f * join_l[col];
+    j.x += f * v.x;
+    j.y += f * v.y;
+  }
+  return j;
+}
+
+// blockIdx.x = ((row * head_tiles + head tile) * heads + head) * slices + slice.
+template <int D, int NT, bool kIds>
+__global__ void __launch_bounds__(kThreads, RingShape<D, NT>::kCtasPerSm)
+    attention_slices_kernel(const __grid_constant__ AttentionParams p) {
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(128) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int slices = (int)cluster.num_blocks(), slice = (int)cluster.block_rank();
+  const unsigned unit = blockIdx.x / (unsigned)slices;
+  const int h = (int)(unit % (unsigned)p.c.heads);
+  const unsigned rest = unit / (unsigned)p.c.heads;
+  const int ht = (int)(rest % (unsigned)p.head_tiles);
+  const int t = (int)(rest / (unsigned)p.head_tiles);
+  const int head0 = h * p.group + ht * 8 * NT;           // first query head of this CTA
+  const int heads = min(8 * NT, p.group - ht * 8 * NT);  // and how many
+
+  grid_dependency_wait();
+  const RowSpan r = row_span<kIds>(p, t);
+  const int tiles = (int)(((int64_t)r.n + kTile - 1) / kTile);
+  const int per = (tiles + slices - 1) / slices;
+  const int tile0 = min(tiles, slice * per), tile1 = min(tiles, tile0 + per);
+  Heads<D, NT> hd;
+  attend_tiles<D, NT, kIds>(p, r, t, h, head0, heads, tile0, tile1, threadIdx.x >> 5, kWarps,
+                            smem, hd);
+  leave_sums<D, NT>(hd, smem);
+
+  const int64_t at = (int64_t)t * p.q_heads + head0;
+  if (slices == 1) {
+    for (int i = threadIdx.x; i < heads * (D / 2); i += kThreads) {
+      const int head = i / (D / 2), d = 2 * (i % (D / 2));
+      write_out<D>(p, at + head, d, join_warps<D, NT>(smem, head, d));
+    }
+    return;
+  }
+  // The CTA's own join goes behind the warps' (each thread its own values),
+  // then every CTA adds its part of the outputs over the cluster.
+  Joined* mine = reinterpret_cast<Joined*>(smem + SliceJoin<D, NT>::kWarpBytes);
+  for (int i = threadIdx.x; i < heads * (D / 2); i += kThreads)
+    mine[i] = join_warps<D, NT>(smem, i / (D / 2), 2 * (i % (D / 2)));
+  cluster.sync();
+  for (int i = slice * kThreads + threadIdx.x; i < heads * (D / 2);
+       i += slices * kThreads) {
+    Joined j{kNoScore, 0.0f, 0.0f, 0.0f};
+    Joined other[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < slices) {
+        other[c] = *cluster.map_shared_rank(mine + i, c);
+        j.top = fmaxf(j.top, other[c].top);
+      }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < slices) {
+        const float f = exp2_approx(other[c].top - j.top);
+        j.sum += f * other[c].sum;
+        j.x += f * other[c].x;
+        j.y += f * other[c].y;
+      }
+    write_out<D>(p, at + i / (D / 2), 2 * (i % (D / 2)), j);
+  }
+  cluster.sync();  // no CTA leaves while others read its shared memory
+}
+
+}  // namespace kv4
+}  // namespace dcp

@@ -218,7 +218,7 @@ static cudaError_t launch_all(const AttentionParams& p, int dim, const Plan& pla
   if (e != cudaSuccess || !p.weights || p.width == 0) return e;
   const int64_t tiles = ((int64_t)p.width + kWeightTokens - 1) / kWeightTokens;
   return launch(p.ids ? weights_kernel<true> : weights_kernel<false>,
-                dim3((unsigned)(p.rows * tiles)), 256, (size_t)p.q_heads * 3 * sizeof(float), 1,
+                dim3((unsigned)(p.rows * tiles)), 256, (size_t)((p.q_heads + 3) & ~3) * 3 * sizeof(float), 1,
                 stream, p);
 }
 
@@ -379,13 +379,13 @@ dcp_status dcp_kv4_evict(const dcp_kv4_cache* cache, const dcp_kv4_evict_args* a
   p.row_scales = cache->heads * cache->dim / kBlock;
   // CTAs per sequence: 8192 weights each, up to a portable cluster
   int ctas = 1;
-  while (ctas < 8 && (int64_t)ctas * 8192 < limit) ctas *= 2;
+  while (ctas < kSelMostCtas && (int64_t)ctas * 8192 < limit) ctas *= 2;
   cudaError_t e = launch(evict_select_kernel, dim3((unsigned)(a->num_seqs * ctas)), kSelThreads, 0,
                          ctas, (cudaStream_t)stream, p);
   if (e != cudaSuccess) return DCP_ERR_CUDA;
   const int64_t items = (int64_t)a->num_seqs * a->budget;
-  e = launch(evict_copy_kernel, dim3((unsigned)((items + 7) / 8)), 256, 0, 1, (cudaStream_t)stream,
-             p);
+  e = launch(evict_copy_kernel, dim3((unsigned)((items + 8 * kCopy - 1) / (8 * kCopy))), 256, 0, 1,
+             (cudaStream_t)stream, p);
   return status_of(e);
 }
 

@@ -502,18 +502,20 @@ __device__ __forceinline__ void write_out(const AttentionParams& p, int64_t at, 
   reinterpret_cast<uint32_t*>(p.out)[(at * D + d) >> 1] = pack_pair(j.x * inv, j.y * inv, p.dtype);
 }
 
-// weights[t][pos] += sum over the query heads of 2^(x - m) / l: 8 lanes per
-// token, a CTA per 1024 tokens of a row.  From m and l rather than lse, whose
-// rounding would be an error of the exponent; the exponent is the attention's
-// own, bit for bit.
-constexpr int kWeightTokens = 1024;
+// weights[t][pos] += sum over the query heads of 2^(x - m) / l, from m and l
+// rather than lse, whose rounding would be an error of the exponent; the
+// exponent is the attention's own, bit for bit.  8 lanes a token, 4 heads to a
+// lane's load where the rows allow it, 4 tokens of a lane in flight; a CTA per
+// 128 tokens of a row.
+constexpr int kWeightTokens = 128;
 
 template <bool kIds>
 __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ AttentionParams p) {
-  extern __shared__ float weight_heads[];  // [3][q_heads]: multiplier, reference, 1 / sum
-  float* mult = weight_heads;
-  float* ref = mult + p.q_heads;
-  float* inv = ref + p.q_heads;
+  extern __shared__ __align__(16) float weight_heads[];  // [q_heads] each, rounded up to 4
+  const int padded = (p.q_heads + 3) & ~3;
+  float* mult = weight_heads;  // multiplier, reference, 1 / sum
+  float* ref = mult + padded;
+  float* inv = ref + padded;
   const int tiles = (p.width + kWeightTokens - 1) / kWeightTokens;
   const int t = blockIdx.x / tiles;
   const int64_t j0 = (int64_t)(blockIdx.x % tiles) * kWeightTokens;
@@ -531,27 +533,56 @@ __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ At
   __syncthreads();
   const int row_start = kIds && p.row_starts ? __ldg(p.row_starts + t) : 0;
   const int sub = threadIdx.x & 7;
-  for (int i = threadIdx.x >> 3; i < kWeightTokens; i += 32) {
-    const int64_t j = j0 + i;
-    float sum = 0.0f;
-    if (j < n) {
-      const float* x = p.scores + ((int64_t)t * p.width + j) * p.q_heads;
-      for (int h = sub; h < p.q_heads; h += 8) {
-        // absent tokens: 2^-inf = 0
-        sum += exp2_approx(fmaf(x[h], mult[h], -ref[h])) * inv[h];
-      }
+  constexpr int kMine = kWeightTokens / 32;  // tokens of a lane
+  const int64_t first = j0 + (threadIdx.x >> 3);
+  float sum[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) sum[i] = 0.0f;
+  // a token beyond the last reads the last
+  const float* x[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    x[i] = p.scores + ((int64_t)t * p.width + min(first + 32 * i, (int64_t)n - 1)) * p.q_heads;
+  // absent tokens: 2^-inf = 0
+  if (p.q_heads % 4 == 0) {
+    for (int h = 4 * sub; h < p.q_heads; h += 32) {
+      const float4 a = *reinterpret_cast<const float4*>(mult + h);
+      const float4 b = *reinterpret_cast<const float4*>(ref + h);
+      const float4 c = *reinterpret_cast<const float4*>(inv + h);
+      float4 v[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) v[i] = *reinterpret_cast<const float4*>(x[i] + h);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        sum[i] += exp2_approx(fmaf(v[i].x, a.x, -b.x)) * c.x +
+                  exp2_approx(fmaf(v[i].y, a.y, -b.y)) * c.y +
+                  exp2_approx(fmaf(v[i].z, a.z, -b.z)) * c.z +
+                  exp2_approx(fmaf(v[i].w, a.w, -b.w)) * c.w;
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-    if (sub == 0 && j < n) {
+  } else {
+    for (int h = sub; h < p.q_heads; h += 8)
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        sum[i] += exp2_approx(fmaf(x[i][h], mult[h], -ref[h])) * inv[h];
+  }
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 4);
+  }
+  if (sub == 0) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int64_t j = first + 32 * i;
+      if (j >= n) continue;
       const int pos = token_pos<kIds>(p, r, t, row_start, (int)j);
       if (pos >= 0 && pos < p.weights_width) {
         float* w = p.weights + (int64_t)t * p.weights_stride + pos;
         if constexpr (kIds)
-          atomicAdd(w, sum);  // an id may be listed twice
+          atomicAdd(w, sum[i]);  // an id may be listed twice
         else
-          *w += sum;
+          *w += sum[i];
       }
     }
   }

@@ -125,6 +125,33 @@ def test_append_writes_exact_codes_and_read_returns_them(dk, dtype, n, heads, di
         assert np.array_equal(got.double().cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("unit", [1.0, 2.0 ** -20, 2.0 ** 20])
+def test_append_codes_of_every_significand(dk, dtype, unit):
+    """Blocks over all scales and all 16-bit significands, midpoints of the grid
+    and their neighbours among them: every code and scale exact."""
+    rng = np.random.default_rng(31)
+    n, dim = 4096, 256
+    scale = ref.SCALES[rng.integers(24, 120, (n, 1, dim // 16, 1))]
+    x = rng.uniform(-6, 6, (n, 1, dim // 16, 16))
+    ties = rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], x.shape) * rng.choice([-1, 1], x.shape)
+    x = np.where(rng.random(x.shape) < 0.5, ties, x)
+    x[..., 0] = 6.0  # the block's scale
+    x = (x * scale * (unit if dtype == "bf16" else 1.0)).reshape(n, 1, dim)
+    t = torch.from_numpy(x).to(TYPES[dtype])
+    near = t.view(torch.int16) + torch.from_numpy(rng.integers(-1, 2, x.shape).astype(np.int16))
+    t = torch.where(torch.from_numpy(rng.random(x.shape) < 0.3), near.view(t.dtype), t).to(DEV)
+    u = unit if dtype == "bf16" else 1.0
+    cache = dk.Kv4Cache.allocate(1, n, 1, dim, DEV, u, u)
+    dk.kv4_append(cache, t, t, torch.arange(n, device=DEV))
+    want_c, want_s = ref.encode(t.double().cpu().numpy(), u)
+    assert np.array_equal(cache.k_scales[0].cpu().numpy(), want_s)
+    want = ref.decode(ref.pack(want_c), want_s)
+    got = ref.decode(cache.k_codes[0].cpu().numpy(), want_s)
+    assert np.array_equal(got, want)
+    assert torch.equal(cache.k_codes, cache.v_codes)
+
+
 def test_append_takes_strided_and_unaligned_values(dk):
     rng = np.random.default_rng(5)
     n, heads, dim = 9, 3, 64
@@ -430,7 +457,8 @@ def test_no_rows_and_no_pages(dk):
 # ---------------------------------------------------------------- eviction
 @pytest.mark.parametrize("lens,budget,sinks,recent", [
     ([100, 64, 65, 0, 1], 64, 4, 16), ([5000, 4999, 31], 32, 0, 0), ([300, 40], 40, 40, 0),
-    ([300, 41], 40, 0, 40), ([20000, 9000], 1000, 7, 33), ([70000], 300, 0, 1), ([9], 1, 0, 0)])
+    ([300, 41], 40, 0, 40), ([20000, 9000], 1000, 7, 33), ([70000], 300, 0, 1), ([9], 1, 0, 0),
+    ([150000, 140001], 2000, 0, 100)])
 @pytest.mark.parametrize("kind", ["ties", "zeros", "spread", "odd"])
 def test_eviction_keeps_the_heaviest_in_order(dk, lens, budget, sinks, recent, kind):
     rng = np.random.default_rng(sum(lens) + budget)

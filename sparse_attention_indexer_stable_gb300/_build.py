@@ -1,13 +1,17 @@
-"""Builds the CUDA library in-tree: csrc/*.cu -> _build/libdcp_topk.so (sm_103a).
+"""Builds the CUDA library in-tree: csrc/*.cu -> _build/libdcp_topk.so (sm_103a),
+and the torch side of the 4-bit cache: csrc/kv4_binding.cpp -> _build/_kv4_binding-*.so.
 
 Plain nvcc, one translation unit per subject compiled side by side, no CMake; host code has no
 architecture-specific flags so the same source builds on x86_64 and aarch64.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -68,3 +72,35 @@ def build(force: bool = False, extra_flags=(), path: str = LIB_PATH) -> str:
 def build_race_check(force: bool = False) -> str:
     """The race-check build (see POISON_LIB_PATH); returns its path."""
     return build(force, POISON_FLAGS, POISON_LIB_PATH)
+
+
+# The torch side of the 4-bit cache's functions: host C++ against torch's
+# headers, so built anew for another torch.
+def binding_path() -> str:
+    return os.path.join(OUT_DIR, f"_kv4_binding-{importlib.metadata.version('torch')}.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/kv4_binding.cpp if missing or older than its sources;
+    returns its path."""
+    path, source = binding_path(), os.path.join(CSRC, "kv4_binding.cpp")
+    headers = [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
+    if not force and os.path.exists(path) and all(
+            os.path.getmtime(f) <= os.path.getmtime(path) for f in [source, *headers]):
+        return path
+    cxx = shutil.which(os.environ.get("CXX", "g++"))
+    if cxx is None:
+        raise RuntimeError("no C++ compiler: set CXX or put g++ on PATH")
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda_dir = os.path.dirname(os.path.dirname(_nvcc()))
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = path + f".{os.getpid()}.tmp"
+    subprocess.check_call([
+        cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
+        "-I", os.path.join(torch_dir, "include"),
+        "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+        "-I", os.path.join(cuda_dir, "include"), "-I", sysconfig.get_paths()["include"],
+        "-o", tmp, source, "-L", os.path.join(torch_dir, "lib"),
+        "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, path)
+    return path

@@ -11,10 +11,13 @@ synchronises the host, and there is no CPU fallback.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
+import importlib.util
 import struct
+import threading
 
-from . import DCP_OK, DcpError, _check, _on_device, _stream_handle, _torch, library
+from . import DCP_OK, DcpError, _build, _check, _torch, library
 
 __all__ = ["Kv4Cache", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_workspace_size",
            "kv4_evict", "DCP_F16", "DCP_BF16", "DCP_F32"]
@@ -25,6 +28,27 @@ DCP_F16, DCP_BF16, DCP_F32 = 0, 1, 2
 _CACHE = struct.Struct("PPPPqiiiff4x")
 _ATTENTION = struct.Struct("PqqPqPPPPqPPqqPPPNiiiiiiiff4x")
 _EVICT = struct.Struct("PqPPqPqPPPiiiiii")
+
+_lock = threading.Lock()
+_bound = None
+
+
+def _bind():
+    """The torch side of these functions (csrc/kv4_binding.cpp), connected to
+    the library."""
+    global _bound
+    with _lock:
+        if _bound is None:
+            _torch()  # loads the libraries that the module is linked against
+            lib = library()
+            spec = importlib.util.spec_from_file_location("_kv4_binding", _build.build_binding())
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.connect(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.dcp_kv4_append, lib.dcp_kv4_read, lib.dcp_kv4_attention_workspace_size,
+                lib.dcp_kv4_attention, lib.dcp_kv4_evict)])
+            _bound = module
+    return _bound
 
 
 @functools.lru_cache(maxsize=None)
@@ -38,17 +62,11 @@ def _raise(status, where):
         raise DcpError(status, where)
 
 
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _allocating(stream, dev):
-    """A context in which torch allocates for `stream`: what a call allocates
-    may then be freed as soon as the call returns."""
-    torch = _torch()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_handle(stream, dev), device=dev)
-    return torch.cuda.stream(stream)
+def _handle(stream):
+    """A raw stream handle, or None for the current stream."""
+    if stream is None:
+        return None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 class Kv4Cache:
@@ -63,7 +81,7 @@ class Kv4Cache:
     """
 
     __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "num_pages", "page_size", "heads",
-                 "dim", "k_unit", "v_unit", "device", "_raw", "_key")
+                 "dim", "k_unit", "v_unit", "device", "_raw")
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales, k_unit=1.0, v_unit=1.0):
         torch = _torch()
@@ -85,7 +103,6 @@ class Kv4Cache:
         self._raw = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
                                 v_scales.data_ptr(), pages, page_size, heads, self.dim,
                                 self.k_unit, self.v_unit)
-        self._key = (pages, page_size, heads, self.dim)
         # an empty append checks the sizes, the units and the alignment
         _raise(library().dcp_kv4_append(self._raw, None, None, DCP_BF16, 0, 0, 0, 0, 0, None,
                                         None), "Kv4Cache")
@@ -101,30 +118,9 @@ class Kv4Cache:
         return cls(*planes, k_unit=k_unit, v_unit=v_unit)
 
 
-def _rows(t, name, dtype, dev, what):
-    """A 2-D tensor whose rows are contiguous (at any stride)."""
-    if not isinstance(t, _torch().Tensor) or t.dtype != dtype or t.get_device() != dev:
-        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{dev}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1 and t.shape[0]):
-        raise ValueError(f"{name} must be {what}, its rows contiguous")
-
-
 def _cache(cache):
     if not isinstance(cache, Kv4Cache):
         raise TypeError("cache must be a Kv4Cache")
-    return cache.device
-
-
-def _values(t, name, cache, dtypes):
-    """(n, heads, dim) values with unit stride along dim, on the cache's device."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-        raise TypeError(f"{name} must be a torch.Tensor of float16, bfloat16"
-                        + (" or float32" if len(dtypes) > 2 else ""))
-    if t.get_device() != cache.device:
-        raise ValueError(f"{name} must be on cuda:{cache.device}")
-    if t.dim() != 3 or t.shape[2] != cache.dim or t.stride(2) != 1:
-        raise ValueError(f"{name} must be 3-D, its last dimension dim = {cache.dim} contiguous")
 
 
 def kv4_append(cache, k, v, slots, stream=None):
@@ -134,67 +130,25 @@ def kv4_append(cache, k, v, slots, stream=None):
     strides; slots: int64 (N,), page * page_size + offset; tokens whose slot is
     outside the cache (for example -1) are skipped.  Slots are distinct.
     """
-    dev = _cache(cache)
-    _values(k, "k", cache, _dtypes())
-    _values(v, "v", cache, _dtypes())
-    if k.dtype != v.dtype or k.shape != v.shape or k.shape[1] != cache.heads:
-        raise ValueError("k and v must both be (N, heads, dim) of one dtype")
-    _check(slots, "slots", _torch().int64, dev)
-    if slots.shape != (k.shape[0],):
-        raise ValueError("slots must be (N,)")
-    kr, kh, _ = k.stride()
-    vr, vh, _ = v.stride()
-    _raise(_on_device(dev, lambda: library().dcp_kv4_append(
-        cache._raw, k.data_ptr(), v.data_ptr(), _dtypes()[k.dtype], k.shape[0], kr, kh, vr, vh,
-        slots.data_ptr(), _stream_handle(stream, dev))), "dcp_kv4_append")
+    _cache(cache)
+    _raise((_bound or _bind()).append(cache._raw, cache.device, k, v, slots, _handle(stream)),
+           "dcp_kv4_append")
 
 
 def kv4_read(cache, slots, dtype=None, k=None, v=None, stream=None):
     """What the slots stand for: (k, v), each (N, heads, dim) of dtype
     (default bfloat16).  Slots outside the cache read as zeros.
     """
-    torch = _torch()
-    dev = _cache(cache)
-    _check(slots, "slots", torch.int64, dev)
-    if slots.dim() != 1:
-        raise ValueError("slots must be (N,)")
+    _cache(cache)
     if dtype is None:
-        dtype = k.dtype if k is not None else torch.bfloat16
+        dtype = _torch().bfloat16 if k is None else k.dtype
     if dtype not in _dtypes():
         raise TypeError("dtype must be float16, bfloat16 or float32")
-    shape = (slots.shape[0], cache.heads, cache.dim)
-    if k is None or v is None:
-        if stream is None:
-            k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
-            v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
-        else:
-            with _allocating(stream, dev):
-                k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
-                v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
-    _check(k, "k", dtype, dev)
-    _check(v, "v", dtype, dev)
-    if k.shape != shape or v.shape != shape:
-        raise ValueError("k and v must be (N, heads, dim)")
-    _raise(_on_device(dev, lambda: library().dcp_kv4_read(
-        cache._raw, k.data_ptr(), v.data_ptr(), _dtypes()[dtype], shape[0], slots.data_ptr(),
-        _stream_handle(stream, dev))), "dcp_kv4_read")
-    return k, v
-
-
-@functools.lru_cache(maxsize=1024)
-def _workspace_size(key, rows, q_heads, num_seqs, table_width, num_ids, max_len, weights):
-    import ctypes
-
-    pages, page_size, heads, dim = key
-    raw = _CACHE.pack(16, 16, 16, 16, pages, page_size, heads, dim, 1.0, 1.0)
-    ids = 0 if num_ids is None else 16
-    args = _ATTENTION.pack(0, 0, 0, 0, 0, 0, 0, 0, ids, 0, 0, 16 if weights else 0, 0, 0, 0, 0, 0,
-                           0, DCP_BF16, rows, q_heads, num_seqs, table_width, num_ids or 0,
-                           max_len, 0.0, 0.0)
-    n = ctypes.c_size_t(0)
-    _raise(library().dcp_kv4_attention_workspace_size(raw, args, ctypes.byref(n)),
-           "dcp_kv4_attention_workspace_size")
-    return n.value
+    r = (_bound or _bind()).read(cache._raw, cache.device, slots, _dtypes()[dtype], k, v,
+                                 _handle(stream))
+    if type(r) is int:
+        _raise(r, "dcp_kv4_read")
+    return r
 
 
 def kv4_attention_workspace_size(cache, rows, q_heads, table_width, num_ids=None, max_len=0,
@@ -202,8 +156,13 @@ def kv4_attention_workspace_size(cache, rows, q_heads, table_width, num_ids=None
     """Workspace bytes of kv4_attention for these sizes (num_ids: None without
     ids); table_width is the block table's pages per sequence."""
     _cache(cache)
-    return _workspace_size(cache._key, rows, q_heads, rows, table_width, num_ids, max_len,
-                           bool(weights))
+    args = _ATTENTION.pack(0, 0, 0, 0, 0, 0, 0, 0, 0 if num_ids is None else 16, 0, 0,
+                           16 if weights else 0, 0, 0, 0, 0, 0, 0, DCP_BF16, rows, q_heads, rows,
+                           table_width, num_ids or 0, max_len, 0.0, 0.0)
+    n = ctypes.c_size_t(0)
+    _raise(library().dcp_kv4_attention_workspace_size(cache._raw, args, ctypes.byref(n)),
+           "dcp_kv4_attention_workspace_size")
+    return n.value
 
 
 def kv4_attention(cache, q, table, lens, ids=None, owner=None, starts=None, row_starts=None,
@@ -230,87 +189,13 @@ def kv4_attention(cache, q, table, lens, ids=None, owner=None, starts=None, row_
     the launch, and lens beyond it are cut there.
     A row that sees nothing gives zeros and lse -inf.
     """
-    torch = _torch()
-    dev = _cache(cache)
-    dtypes = _dtypes()
-    if isinstance(q, torch.Tensor) and q.dtype == torch.float32:
-        raise TypeError("q must be a torch.Tensor of float16, bfloat16")
-    _values(q, "q", cache, dtypes)
-    T, heads, dim = q.shape
-    if heads < 1 or heads % cache.heads:
-        raise ValueError("q's heads must be a multiple of the cache's heads")
-    int32 = torch.int32
-    _rows(table, "table", int32, dev, "(sequences, pages)")
-    _check(lens, "lens", int32, dev)
-    if lens.shape != (T,):
-        raise ValueError("lens must be (T,)")
-    for name, t in (("starts", starts), ("owner", owner), ("row_starts", row_starts)):
-        if t is not None:
-            _check(t, name, int32, dev)
-            if t.shape != (T,):
-                raise ValueError(f"{name} must be (T,)")
-    num_seqs, width = table.shape
-    if owner is None and num_seqs < T:
-        raise ValueError("table must have a row for each row of q (or give owner)")
-    num_ids, ids_ptr, ids_stride = None, 0, 0
-    if ids is not None:
-        _rows(ids, "ids", int32, dev, "(T, K)")
-        if ids.shape[0] != T:
-            raise ValueError("ids must be (T, K)")
-        num_ids, ids_stride = ids.shape[1], ids.stride(0)
-        # no ids at all (K = 0) have no address, and a null one means every
-        # position; nothing is read from this one
-        ids_ptr = ids.data_ptr() or lens.data_ptr()
-    w_stride = w_width = 0
-    if weights is not None:
-        _rows(weights, "weights", torch.float32, dev, "(T, positions)")
-        if owner is not None:
-            raise ValueError("weights need one row per sequence: not with owner")
-        if weights.shape[0] != T:
-            raise ValueError("weights must be (T, positions)")
-        w_stride, w_width = weights.stride(0), weights.shape[1]
-        if T > 1 and w_stride < w_width:
-            raise ValueError("the rows of weights must not overlap")
-    if not softcap >= 0.0:
-        raise ValueError("softcap must not be negative")
-    need = _workspace_size(cache._key, T, heads, num_seqs, width, num_ids, max_len,
-                           weights is not None)
-    if out is None or lse is None or (need and workspace is None):
-        if stream is None:
-            out, lse, workspace = _outputs(torch, q, T, heads, dim, dev, need, out, lse,
-                                           workspace)
-        else:
-            with _allocating(stream, dev):
-                out, lse, workspace = _outputs(torch, q, T, heads, dim, dev, need, out, lse,
-                                               workspace)
-    _check(out, "out", q.dtype, dev)
-    _check(lse, "lse", torch.float32, dev)
-    if out.shape != (T, heads, dim) or lse.shape != (T, heads):
-        raise ValueError("out must be (T, q_heads, dim) and lse (T, q_heads)")
-    have = 0
-    if workspace is not None:
-        _check(workspace, "workspace", torch.uint8, dev)
-        have = workspace.numel()
-        if have < need:
-            raise ValueError(f"workspace must hold {need} bytes")
-    args = _ATTENTION.pack(
-        q.data_ptr(), q.stride(0), q.stride(1), table.data_ptr(), table.stride(0),
-        lens.data_ptr(), _ptr(starts), _ptr(owner), ids_ptr, ids_stride, _ptr(row_starts),
-        _ptr(weights), w_stride, w_width, out.data_ptr(), lse.data_ptr(), _ptr(workspace), have,
-        dtypes[q.dtype], T, heads, num_seqs, width, num_ids or 0, max_len, scale or 0.0, softcap)
-    _raise(_on_device(dev, lambda: library().dcp_kv4_attention(
-        cache._raw, args, _stream_handle(stream, dev))), "dcp_kv4_attention")
-    return out, lse
-
-
-def _outputs(torch, q, T, heads, dim, dev, need, out, lse, workspace):
-    if out is None:
-        out = torch.empty((T, heads, dim), dtype=q.dtype, device=dev)
-    if lse is None:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return out, lse, workspace
+    _cache(cache)
+    r = (_bound or _bind()).attention(cache._raw, cache.device, q, table, lens, ids, owner, starts,
+                                      row_starts, scale, softcap, weights, max_len, out, lse,
+                                      workspace, _handle(stream))
+    if type(r) is int:
+        _raise(r, "dcp_kv4_attention")
+    return r
 
 
 def kv4_evict(cache, table, lens, weights, out_table, budget, sinks=0, recent=0, kept=None,
@@ -326,51 +211,10 @@ def kv4_evict(cache, table, lens, weights, out_table, budget, sinks=0, recent=0,
     Returns (kept int32 (sequences, budget): the kept positions, ascending, then
     -1; out_lens int32; out_weights float32 (sequences, budget)).
     """
-    torch = _torch()
-    dev = _cache(cache)
-    int32 = torch.int32
-    budget, sinks, recent = int(budget), int(sinks), int(recent)
-    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
-        raise ValueError("need budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget")
-    _rows(table, "table", int32, dev, "(sequences, pages)")
-    _rows(out_table, "out_table", int32, dev, "(sequences, pages)")
-    _rows(weights, "weights", torch.float32, dev, "(sequences, positions)")
-    B, width = table.shape
-    if weights.shape[0] != B or out_table.shape[0] != B:
-        raise ValueError("table, weights and out_table must have a row for each sequence")
-    if out_table.shape[1] * cache.page_size < budget:
-        raise ValueError("out_table must have ceil(budget / page_size) pages for each sequence")
-    _check(lens, "lens", int32, dev)
-    if lens.shape != (B,):
-        raise ValueError("lens must have an entry for each sequence")
-    if kept is None or out_lens is None or out_weights is None:
-        if stream is None:
-            kept, out_lens, out_weights = _kept(torch, B, budget, dev, kept, out_lens,
-                                                out_weights)
-        else:
-            with _allocating(stream, dev):
-                kept, out_lens, out_weights = _kept(torch, B, budget, dev, kept, out_lens,
-                                                    out_weights)
-    _check(kept, "kept", int32, dev)
-    _check(out_lens, "out_lens", int32, dev)
-    _check(out_weights, "out_weights", torch.float32, dev)
-    if (kept.shape != (B, budget) or out_weights.shape != (B, budget)
-            or out_lens.shape != (B,)):
-        raise ValueError("kept and out_weights must be (sequences, budget), out_lens (sequences,)")
-    args = _EVICT.pack(table.data_ptr(), table.stride(0), lens.data_ptr(), weights.data_ptr(),
-                       weights.stride(0), out_table.data_ptr(), out_table.stride(0),
-                       kept.data_ptr(), out_lens.data_ptr(), out_weights.data_ptr(), B, width,
-                       weights.shape[1], budget, sinks, recent)
-    _raise(_on_device(dev, lambda: library().dcp_kv4_evict(
-        cache._raw, args, _stream_handle(stream, dev))), "dcp_kv4_evict")
-    return kept, out_lens, out_weights
-
-
-def _kept(torch, B, budget, dev, kept, out_lens, out_weights):
-    if kept is None:
-        kept = torch.empty((B, budget), dtype=torch.int32, device=dev)
-    if out_lens is None:
-        out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-    if out_weights is None:
-        out_weights = torch.empty((B, budget), dtype=torch.float32, device=dev)
-    return kept, out_lens, out_weights
+    _cache(cache)
+    r = (_bound or _bind()).evict(cache._raw, cache.device, table, lens, weights, out_table,
+                                  budget, sinks, recent, kept, out_lens, out_weights,
+                                  _handle(stream))
+    if type(r) is int:
+        _raise(r, "dcp_kv4_evict")
+    return r

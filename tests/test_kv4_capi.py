@@ -119,6 +119,20 @@ def test_null_arguments():
     assert lib.dcp_kv4_attention_workspace_size(cache(), attention(), None) == dk.DCP_ERR_INVALID
 
 
+def test_the_binding_loads_and_refuses_what_is_no_cache():
+    """The torch side is built against this torch and connected to the library."""
+    binding = kv4._bind()
+    with pytest.raises(TypeError):
+        binding.append(b"", 0, None, None, None, None)
+    with pytest.raises(TypeError):
+        binding.append(cache())
+    for call in (lambda: dk.kv4_append(None, None, None, None), lambda: dk.kv4_read(None, None),
+                 lambda: dk.kv4_attention(None, None, None, None),
+                 lambda: dk.kv4_evict(None, None, None, None, None, 1)):
+        with pytest.raises(TypeError):
+            call()
+
+
 def test_reference_grid_and_rounding():
     """The reference's own arithmetic: grid values, ties to even, saturation."""
     assert ref.SCALES[1] == 2.0 ** -9 and ref.SCALES[126] == 448 and ref.SCALES[56] == 1.0

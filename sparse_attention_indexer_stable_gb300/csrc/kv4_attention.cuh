@@ -356,7 +356,7 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
 #pragma unroll
       for (int u = 0; u < kSub; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][u][e] = cap * tanhf(s[n][u][e] * hd.mult[n][e & 1]);
+        for (int e = 0; e < 4; ++e) s[n][u][e] = cap * tanh_score(s[n][u][e] * hd.mult[n][e & 1]);
   }
   if (mask != 0xffffffffu) {
 #pragma unroll

@@ -2,12 +2,15 @@
 //
 // Choice: the budget - sinks - recent largest weights of the middle, ties to
 // the lowest position, as a set in position order, so nothing is sorted.  A
-// cluster of CTAs takes a sequence, each CTA a slice of the middle: three
-// digit histograms (11, 11, 10 bits) of order-preserving 32-bit keys, added
-// over the cluster through distributed shared memory, give the smallest kept
-// key and how many of its ties stay; counts per warp and CTA then give every
-// kept token its place.  Bound by the latency of its passes over weights that
-// sit in L2 after the first.
+// cluster of CTAs takes a sequence, each CTA a slice of it and each thread 16
+// weights in a row.  Four digit histograms (8 bits) of order-preserving 32-bit
+// keys, added over the cluster through distributed shared memory, give the
+// smallest kept key and how many of its ties stay; counts per thread then give
+// every kept token its place.  Bound by the latency of its passes: with 32
+// copies of a histogram, one for each lane, no two lanes of a warp meet (equal
+// weights are common, and shared-memory atomics on one address follow one
+// another); 2048 bins in one copy took twice as long, and grouping equal lanes
+// first (__match_any_sync) longer still.
 //
 // Copy: a warp per four kept tokens, their loads together.  Bound by memory.
 #pragma once
@@ -21,9 +24,10 @@ namespace kv4 {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 2048;
+constexpr int kSelBins = 256;
 constexpr int kSelKeys = 16;     // weights of a thread at a time
 constexpr int kSelMostCtas = 8;  // of a cluster
+constexpr int kSelRound = kSelThreads * kSelKeys;
 
 struct EvictParams {
   Planes c;
@@ -51,9 +55,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 struct SelectState {
-  uint32_t hist[3][kSelBins];  // one per pass: a CTA may still read one while the next fills
-  uint32_t warp_sum[kSelWarps];
-  uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+  union {
+    uint32_t hist[kSelBins][32];  // a copy for each lane
+    uint16_t list[kSelRound];     // a round's kept weights, by their place in the round
+  };
+  uint32_t sums[4][kSelBins];    // the CTA's histogram, one per pass: others may still read one
+  uint32_t warp_sum[kSelWarps], warp_eq[kSelWarps];
   uint32_t digit, above;
   uint32_t cta_gt, cta_eq;
 };
@@ -67,6 +74,32 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
   return v;  // inclusive
 }
 
+// Keys of the weights [at, at + 16) of a row; beyond [lo, hi) none (bit i of
+// the result: key i counts).
+__device__ __forceinline__ uint32_t load_keys(const float* w, int64_t at, int lo, int hi, bool vec,
+                                              uint32_t (&key)[kSelKeys]) {
+  if (vec && at >= lo && at + kSelKeys <= hi) {
+    float4 x[kSelKeys / 4];
+#pragma unroll
+    for (int i = 0; i < kSelKeys / 4; ++i)
+      x[i] = __ldg(reinterpret_cast<const float4*>(w + at) + i);
+#pragma unroll
+    for (int i = 0; i < kSelKeys / 4; ++i) {
+      key[4 * i] = weight_key(x[i].x), key[4 * i + 1] = weight_key(x[i].y);
+      key[4 * i + 2] = weight_key(x[i].z), key[4 * i + 3] = weight_key(x[i].w);
+    }
+    return 0xffffu;
+  }
+  uint32_t in = 0u;
+#pragma unroll
+  for (int i = 0; i < kSelKeys; ++i) {
+    const bool here = at + i >= lo && at + i < hi;
+    key[i] = here ? weight_key(__ldg(w + at + i)) : 0u;
+    in |= (uint32_t)here << i;
+  }
+  return in;
+}
+
 __global__ void __launch_bounds__(kSelThreads, 1)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
   namespace cg = cooperative_groups;
@@ -75,7 +108,6 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / ctas;
-  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&s.hist[0][0])[i] = 0u;
 
   grid_dependency_wait();
   const int n = max(0, min(__ldg(p.lens + b), p.limit));
@@ -91,128 +123,152 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     }
     return;
   }
+
+  // The middle [lo, hi): an equal slice for each CTA, whole pieces of 16, in
+  // rounds of 16 weights a thread.  One round stays in registers, more are read
+  // again in each pass (they are in L2).
+  const int lo = p.sinks, hi = n - p.recent;
+  const int need = p.budget - p.sinks - p.recent;  // fewer than the middle has
+  const int first = lo & ~(kSelKeys - 1);
+  const int64_t slice =
+      ((int64_t)(hi - first) + (int64_t)ctas * kSelKeys - 1) / ((int64_t)ctas * kSelKeys) * kSelKeys;
+  const int rounds = (int)((slice + kSelRound - 1) / kSelRound);
+  const int64_t begin = first + rank * slice;
+  const int end = (int)min((int64_t)hi, begin + slice);  // of this CTA
+  const int64_t mine = begin + (int64_t)tid * kSelKeys;
+  const bool vec = ((uintptr_t)w & 15u) == 0;
+  uint32_t key[kSelKeys];
+  uint32_t in = 0u;
+  auto load = [&](int round) {
+    in = load_keys(w, mine + (int64_t)round * kSelRound, lo, end, vec, key);
+  };
+  if (need > 0) load(0);
+
+  uint32_t prefix = 0u, left = (uint32_t)need;
+#pragma unroll 1
+  for (int pass = 0; pass < 4 && need > 0; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = tid; i < kSelBins * 32 / 4; i += kSelThreads)
+      reinterpret_cast<uint4*>(&s.hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) load(round);
+      if (!__any_sync(0xffffffffu, in != 0u)) continue;
+#pragma unroll
+      for (int i = 0; i < kSelKeys; ++i) {
+        // the digits before this one agree (none before the first)
+        const bool take = ((in >> i) & 1u) && (((key[i] ^ prefix) >> shift) >> 8) == 0u;
+        if (take) atomicAdd(&s.hist[(key[i] >> shift) & 255u][lane], 1u);
+      }
+    }
+    __syncthreads();
+    // the 32 copies: a warp per bin
+#pragma unroll
+    for (int i = 0; i < kSelBins / kSelWarps; ++i) {
+      const int bin = i * kSelWarps + warp;
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, s.hist[bin][lane]);
+      if (lane == 0) s.sums[pass][bin] = sum;
+    }
+    cluster.sync();
+    // over the cluster, a thread per bin in descending order; the first warps
+    uint32_t h = 0u, incl = 0u;
+    if (tid < kSelBins) {
+#pragma unroll
+      for (int c = 0; c < kSelMostCtas; ++c)
+        if (c < ctas) h += *cluster.map_shared_rank(&s.sums[pass][kSelBins - 1 - tid], c);
+      incl = warp_scan(h, lane);
+      if (lane == 31) s.warp_sum[warp] = incl;
+    }
+    __syncthreads();
+    if (tid < kSelBins) {
+      uint32_t before = incl - h;
+      for (int v = 0; v < warp; ++v) before += s.warp_sum[v];
+      if (before < left && left <= before + h)
+        s.digit = (uint32_t)(kSelBins - 1 - tid), s.above = before;
+    }
+    __syncthreads();
+    prefix |= s.digit << shift;
+    left -= s.above;
+  }
+  // `prefix` is the smallest kept key, `left` how many of its ties are kept
+
+  if (need > 0) {
+    // how many above it and how many ties: this thread's, the CTA's
+    auto count = [&](uint32_t& gt, uint32_t& eq) {
+      gt = eq = 0u;
+#pragma unroll
+      for (int i = 0; i < kSelKeys; ++i) {
+        gt += ((in >> i) & 1u) && key[i] > prefix;
+        eq += ((in >> i) & 1u) && key[i] == prefix;
+      }
+    };
+    uint32_t gt, eq, sum_gt = 0u, sum_eq = 0u;
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) load(round);
+      count(gt, eq);
+      sum_gt += gt, sum_eq += eq;
+    }
+    sum_gt = __reduce_add_sync(0xffffffffu, sum_gt);
+    sum_eq = __reduce_add_sync(0xffffffffu, sum_eq);
+    __syncthreads();  // warp_sum has been read
+    if (lane == 0) s.warp_sum[warp] = sum_gt, s.warp_eq[warp] = sum_eq;
+    __syncthreads();
+    if (warp == 0) {
+      sum_gt = __reduce_add_sync(0xffffffffu, s.warp_sum[lane]);
+      sum_eq = __reduce_add_sync(0xffffffffu, s.warp_eq[lane]);
+      if (lane == 0) s.cta_gt = sum_gt, s.cta_eq = sum_eq;
+    }
+    cluster.sync();
+    uint32_t base_gt = 0u, base_eq = 0u;  // before this CTA, then before this round
+#pragma unroll
+    for (int c = 0; c < kSelMostCtas; ++c)
+      if (c < rank) {
+        base_gt += *cluster.map_shared_rank(&s.cta_gt, c);
+        base_eq += *cluster.map_shared_rank(&s.cta_eq, c);
+      }
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) {
+        load(round);
+        count(gt, eq);
+      }
+      const uint32_t incl_gt = warp_scan(gt, lane), incl_eq = warp_scan(eq, lane);
+      __syncthreads();  // the last round's sums have been read
+      if (lane == 31) s.warp_sum[warp] = incl_gt, s.warp_eq[warp] = incl_eq;
+      __syncthreads();
+      const uint32_t warps_gt = warp_scan(s.warp_sum[lane], lane);
+      const uint32_t warps_eq = warp_scan(s.warp_eq[lane], lane);
+      uint32_t at_gt = base_gt + incl_gt - gt, at_eq = base_eq + incl_eq - eq;
+      const uint32_t before_gt = __shfl_sync(0xffffffffu, warps_gt, (warp + 31) & 31);
+      const uint32_t before_eq = __shfl_sync(0xffffffffu, warps_eq, (warp + 31) & 31);
+      if (warp > 0) at_gt += before_gt, at_eq += before_eq;
+      // The round's kept ones into a list, and from there to the outputs: side
+      // by side, where the threads' own places would scatter.
+      const uint32_t base = base_gt + min(base_eq, left);
+      base_gt += __shfl_sync(0xffffffffu, warps_gt, 31);
+      base_eq += __shfl_sync(0xffffffffu, warps_eq, 31);
+#pragma unroll
+      for (int i = 0; i < kSelKeys; ++i) {
+        const bool above = ((in >> i) & 1u) && key[i] > prefix;
+        const bool tie = ((in >> i) & 1u) && key[i] == prefix;
+        if (above || (tie && at_eq < left))
+          s.list[at_gt + min(at_eq, left) - base] = (uint16_t)(tid * kSelKeys + i);
+        at_gt += above;
+        at_eq += tie;
+      }
+      __syncthreads();
+      const int count_kept = (int)(base_gt + min(base_eq, left) - base);
+      const int64_t from = begin + (int64_t)round * kSelRound;
+      for (int j = tid; j < count_kept; j += kSelThreads) {
+        const int64_t pos = from + s.list[j];
+        kept[p.sinks + base + j] = (int32_t)pos;
+        out_w[p.sinks + base + j] = __ldg(w + pos);
+      }
+    }
+  }
   for (int j = all; j < p.sinks; j += stride) kept[j] = j, out_w[j] = w[j];
   for (int j = all; j < p.recent; j += stride) {
     kept[p.budget - p.recent + j] = n - p.recent + j;
     out_w[p.budget - p.recent + j] = w[n - p.recent + j];
-  }
-  const int need = p.budget - p.sinks - p.recent;  // fewer than the middle has
-  if (need == 0) return;
-
-  // This CTA's slice of the middle, and this warp's of that: groups of 16
-  // weights a lane, 32 apart, loaded together.  A slice of one group per warp
-  // stays in registers, a longer one is read again in each pass (it is in L2).
-  const int lo = p.sinks, hi = n - p.recent;
-  constexpr int kGroup = kSelKeys * 32, kRound = kGroup * kSelWarps;
-  const int rounds = ((hi - lo + ctas - 1) / ctas + kRound - 1) / kRound;
-  const int64_t warp0 = lo + ((int64_t)rank * kSelWarps + warp) * rounds * kGroup;
-  float v[kSelKeys];
-  auto load = [&](int round) {
-    const int64_t at = warp0 + (int64_t)round * kGroup + lane;
-#pragma unroll
-    for (int i = 0; i < kSelKeys; ++i)
-      v[i] = at + 32 * i < hi ? __ldg(w + at + 32 * i) : 0.0f;
-  };
-  auto in = [&](int round, int i) {
-    return warp0 + (int64_t)round * kGroup + 32 * i + lane < hi;
-  };
-  load(0);
-  __syncthreads();  // hist is zero
-
-  uint32_t prefix = 0u, left = (uint32_t)need;
-  // digits from the top: bits [21, 32), [10, 21), [0, 10)
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bits = pass == 2 ? 10 : 11;
-    for (int round = 0; round < rounds; ++round) {
-      if (rounds > 1) load(round);
-#pragma unroll
-      for (int i = 0; i < kSelKeys; ++i) {
-        const uint32_t key = weight_key(v[i]);
-        // key >> 32 would be undefined: the first pass takes everything
-        const bool take = in(round, i) &&
-                          (pass == 0 || (key >> (shift + bits)) == (prefix >> (shift + bits)));
-        if (!__any_sync(0xffffffffu, take)) continue;
-        // lanes of one bin add up first: accumulated weights tie a lot
-        const uint32_t bin = take ? (key >> shift) & ((1u << bits) - 1u) : 0xffffffffu;
-        const unsigned same = __match_any_sync(0xffffffffu, bin);
-        if (take && lane == __ffs(same) - 1)
-          atomicAdd(&s.hist[pass][bin], (uint32_t)__popc(same));
-      }
-    }
-    cluster.sync();
-    // bins in descending order, two per thread, added over the cluster
-    const int b0 = kSelBins - 2 - 2 * tid;  // and b0 + 1 before it
-    uint2 h = make_uint2(0u, 0u);
-#pragma unroll
-    for (int c = 0; c < kSelMostCtas; ++c)
-      if (c < ctas) {
-        const uint2 x =
-            *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s.hist[pass][b0], c));
-        h.x += x.x, h.y += x.y;
-      }
-    const uint32_t incl = warp_scan(h.x + h.y, lane);
-    if (lane == 31) s.warp_sum[warp] = incl;
-    __syncthreads();
-    const uint32_t sums = warp_scan(s.warp_sum[lane], lane);
-    const uint32_t before_warp = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
-    const uint32_t before = (warp ? before_warp : 0u) + incl - (h.x + h.y);
-    if (before < left && left <= before + h.y) s.digit = (uint32_t)b0 + 1u, s.above = before;
-    if (before + h.y < left && left <= before + h.y + h.x)
-      s.digit = (uint32_t)b0, s.above = before + h.y;
-    __syncthreads();
-    prefix |= s.digit << shift;
-    left -= s.above;
-    __syncthreads();  // digit and warp_sum have been read
-  }
-  // `prefix` is the smallest kept key, `left` how many of its ties are kept
-
-  uint32_t gt = 0u, eq = 0u;
-  for (int round = 0; round < rounds; ++round) {
-    if (rounds > 1) load(round);
-#pragma unroll
-    for (int i = 0; i < kSelKeys; ++i) {
-      const uint32_t key = weight_key(v[i]);
-      gt += __popc(__ballot_sync(0xffffffffu, in(round, i) && key > prefix));
-      eq += __popc(__ballot_sync(0xffffffffu, in(round, i) && key == prefix));
-    }
-  }
-  if (lane == 0) s.warp_gt[warp] = gt, s.warp_eq[warp] = eq;
-  __syncthreads();
-  // this warp's counts of the warps before it, and the CTA's
-  const uint32_t gt_to = warp_scan(s.warp_gt[lane], lane), eq_to = warp_scan(s.warp_eq[lane], lane);
-  if (warp == 0 && lane == 31) s.cta_gt = gt_to, s.cta_eq = eq_to;
-  cluster.sync();
-  gt = __shfl_sync(0xffffffffu, gt_to, (warp + 31) & 31);
-  eq = __shfl_sync(0xffffffffu, eq_to, (warp + 31) & 31);
-  if (warp == 0) gt = eq = 0u;
-  uint32_t cta_gt = 0u, cta_eq = 0u;
-#pragma unroll
-  for (int c = 0; c < kSelMostCtas; ++c)
-    if (c < rank) {
-      cta_gt += *cluster.map_shared_rank(&s.cta_gt, c);
-      cta_eq += *cluster.map_shared_rank(&s.cta_eq, c);
-    }
-  gt += cta_gt, eq += cta_eq;
-  for (int round = 0; round < rounds; ++round) {
-    if (rounds > 1) load(round);
-#pragma unroll
-    for (int i = 0; i < kSelKeys; ++i) {
-      const uint32_t key = weight_key(v[i]);
-      const bool here = in(round, i);
-      const unsigned is_gt = __ballot_sync(0xffffffffu, here && key > prefix);
-      const unsigned is_eq = __ballot_sync(0xffffffffu, here && key == prefix);
-      const unsigned below = (1u << lane) - 1u;
-      const uint32_t my_eq = eq + __popc(is_eq & below);
-      if (here && (key > prefix || (key == prefix && my_eq < left))) {
-        const uint32_t at = p.sinks + gt + __popc(is_gt & below) + min(my_eq, left);
-        kept[at] = (int32_t)(warp0 + (int64_t)round * kGroup + 32 * i + lane);
-        out_w[at] = v[i];
-      }
-      gt += __popc(is_gt);
-      eq += __popc(is_eq);
-    }
   }
   cluster.sync();  // no CTA leaves while others read its shared memory
 }

@@ -68,13 +68,14 @@ static cudaError_t allow_smem(Kernel* kernel, int bytes) {
 
 template <int D, int NT>
 static cudaError_t allow_attention() {
-  constexpr int kBytes = RingShape<D, NT>::kSmem;
+  constexpr int kSlice = kSliceWarps * RingShape<D, NT>::kBytes;
+  constexpr int kShare = ShareShape<D, NT>::kSmem;
   cudaError_t e;
-  if ((e = allow_smem(attention_slices_kernel<D, NT, false>, kBytes)) != cudaSuccess ||
-      (e = allow_smem(attention_slices_kernel<D, NT, true>, kBytes)) != cudaSuccess ||
-      (e = allow_smem(attention_shares_kernel<D, NT, false>, kBytes)) != cudaSuccess)
+  if ((e = allow_smem(attention_slices_kernel<D, NT, false>, kSlice)) != cudaSuccess ||
+      (e = allow_smem(attention_slices_kernel<D, NT, true>, kSlice)) != cudaSuccess ||
+      (e = allow_smem(attention_shares_kernel<D, NT, false>, kShare)) != cudaSuccess)
     return e;
-  return allow_smem(attention_shares_kernel<D, NT, true>, kBytes);
+  return allow_smem(attention_shares_kernel<D, NT, true>, kShare);
 }
 
 // Per-device kernel attributes, set once (the first call on a device must
@@ -103,7 +104,8 @@ struct Plan {
   int slices;  // CTAs of a row and head, when > 0
   int shares;  // even shares, when > 0
   int together;  // key/value heads that a share walks at the same time
-  size_t records, part_out, part_ml, scores, row_mult, row_ml, bytes;
+  int cuts;    // units, where a CTA joins one head of a unit (0: a warp does)
+  size_t records, cut_at, part_out, part_ml, scores, row_mult, row_ml, bytes;
 };
 
 // The SM count that a call is cut up for: the workspace's size may not depend
@@ -133,26 +135,29 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   // are on the device: both are judged at the longest row.
   const int64_t units = (int64_t)a->rows * c->heads * plan->head_tiles;
   const int64_t tiles = ((int64_t)plan->width + kTile - 1) / kTile;
-  const bool wide = c->dim * plan->heads_per_cta >= 2048;  // one CTA per SM
-  const int64_t slots = kPlanSms * (wide ? 1 : 2);
+  const int64_t warps = c->dim * plan->heads_per_cta >= 2048 ? 8 : 16;  // of an SM
   auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   int64_t least = INT64_MAX;
   for (int s = 1; s <= 8; s *= 2) {
-    const int64_t steps = ceil_div(units * s, slots) *
-                          (ceil_div(ceil_div(tiles, s), kWarps) + kPieceCost);
+    const int64_t steps = ceil_div(units * s, kPlanSms * warps / kSliceWarps) *
+                          (ceil_div(ceil_div(tiles, s), kSliceWarps) + kPieceCost);
     if (steps < least) least = steps, plan->slices = s;
   }
   // the largest power of two that leaves at most a fifth of the warps idle
-  plan->together = kWarps;
+  plan->together = kMostTogether;
   while (ceil_div(c->heads, plan->together) * plan->together * 4 > c->heads * 5)
     plan->together /= 2;
   const int64_t padded = units / c->heads * ceil_div(c->heads, plan->together) * plan->together;
   plan->shares = 0;
-  if (ceil_div(padded * tiles, slots * kWarps) + kPieceCost + kShareCost < least) {
+  if (ceil_div(padded * tiles, kPlanSms * warps) + kPieceCost + kShareCost < least) {
     plan->slices = 0;
-    plan->shares = (int)slots;
+    plan->shares = (int)(kPlanSms * warps / kSliceWarps);  // as many CTAs of 8 warps as fit
   }
-  if (units * 8 > INT_MAX || units * (tiles + 1) / kPlanSms > INT_MAX || (int64_t)a->rows * a->q_heads > INT_MAX) return DCP_ERR_UNSUPPORTED;
+  // A unit is cut into about shares / (rows * units) pieces: from 16 on, two
+  // for each warp of a CTA, a CTA joins one head, otherwise a warp does.
+  const int64_t cuts = a->rows * ceil_div(c->heads, plan->together) * plan->head_tiles;
+  plan->cuts = cuts * 16 <= plan->shares ? (int)cuts : 0;
+  if (units * 8 > INT_MAX || units * (tiles + kPieceTiles + 1) / kPlanSms > INT_MAX || (int64_t)a->rows * a->q_heads > INT_MAX) return DCP_ERR_UNSUPPORTED;
   const size_t heads = (size_t)a->rows * a->q_heads;
   size_t at = 0;
   auto take = [&at](size_t bytes) {
@@ -160,11 +165,12 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
     at += (bytes + 15) & ~(size_t)15;
     return here;
   };
-  plan->records = plan->part_out = plan->part_ml = plan->scores = 0;
+  plan->records = plan->cut_at = plan->part_out = plan->part_ml = plan->scores = 0;
   plan->row_mult = plan->row_ml = 0;
   if (plan->shares) {
     const size_t pieces = (size_t)plan->shares * 2 * plan->together * plan->heads_per_cta;
     plan->records = take(plan->shares * sizeof(int4));
+    plan->cut_at = take(plan->cuts * sizeof(int2));
     plan->part_out = take(pieces * c->dim * sizeof(float));
     plan->part_ml = take(pieces * sizeof(float2));
   }
@@ -180,28 +186,25 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
 template <int D, int NT>
 static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
                                     cudaStream_t stream) {
-  constexpr int kBytes = RingShape<D, NT>::kSmem;
   if (plan.slices) {
     const unsigned grid = (unsigned)p.rows * p.head_tiles * p.c.heads * plan.slices;
     return launch(p.ids ? attention_slices_kernel<D, NT, true>
                         : attention_slices_kernel<D, NT, false>,
-                  dim3(grid), kThreads, kBytes, plan.slices, stream, p);
+                  dim3(grid), kSliceThreads, kSliceWarps * RingShape<D, NT>::kBytes, plan.slices,
+                  stream, p);
   }
-  const cudaError_t e = launch(p.ids ? attention_shares_kernel<D, NT, true>
-                                     : attention_shares_kernel<D, NT, false>,
-                               dim3((unsigned)plan.shares), kThreads, kBytes, 1, stream, p);
+  using Shape = ShareShape<D, NT>;
+  const cudaError_t e =
+      launch(p.ids ? attention_shares_kernel<D, NT, true> : attention_shares_kernel<D, NT, false>,
+             dim3((unsigned)plan.shares), Shape::kThreads, Shape::kSmem, 1, stream, p);
   if (e != cudaSuccess) return e;
-  const int units = (p.c.heads + p.together - 1) / p.together * p.head_tiles;
   const int heads = p.together * 8 * NT;
-  // a unit is cut into about shares / (rows * units) pieces: from 16 on, two
-  // for each warp of a CTA, a CTA joins one head, otherwise a warp does
-  if ((int64_t)p.rows * units * 16 <= plan.shares)
-    return launch(join_shares_kernel<D, NT, true>,
-                  dim3((unsigned)(p.rows * units), (unsigned)heads), 32 * kJoinWarps, 0, 1, stream,
-                  p, plan.shares);
-  return launch(join_shares_kernel<D, NT, false>,
-                dim3((unsigned)plan.shares, (unsigned)(heads / kJoinWarps)), 32 * kJoinWarps, 0, 1,
-                stream, p, plan.shares);
+  return plan.cuts ? launch(join_shares_kernel<D, NT, true>,
+                            dim3((unsigned)plan.cuts, (unsigned)heads), 32 * kJoinWarps, 0, 1,
+                            stream, p)
+                   : launch(join_shares_kernel<D, NT, false>,
+                            dim3((unsigned)plan.shares, (unsigned)(heads / kJoinWarps)),
+                            32 * kJoinWarps, 0, 1, stream, p);
 }
 
 static cudaError_t launch_all(const AttentionParams& p, int dim, const Plan& plan,
@@ -316,6 +319,7 @@ dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
   if (plan.shares) {
     p.shares = reinterpret_cast<int4*>(ws + plan.records);
+    if (plan.cuts) p.cuts = reinterpret_cast<int2*>(ws + plan.cut_at);
     p.part_out = reinterpret_cast<float*>(ws + plan.part_out);
     p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
   }

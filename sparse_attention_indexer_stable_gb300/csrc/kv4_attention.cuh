@@ -56,6 +56,7 @@ struct AttentionParams {
   void* out;
   float* lse;
   int4* shares;       // even shares, [share]: see kv4_shares.cuh
+  int2* cuts;         // and [rows][units], where those are few: a unit's first and last share
   float* part_out;    // [share][2][together][8 * NT][dim]: outputs of its first and last piece
   float2* part_ml;    // [share][2][together][8 * NT]: their references and sums
   // when weights are wanted:
@@ -92,60 +93,85 @@ __device__ __forceinline__ RowSpan row_span(const AttentionParams& p, int t) {
   return r;
 }
 
-// Position of the row's j-th token; -1: absent.
+// The position that the row's j-th token or id stands for, -1: none of the
+// row's.  `given`: the id; without ids j itself.
 template <bool kIds>
-__device__ __forceinline__ int token_pos(const AttentionParams& p, const RowSpan& r, int t,
-                                         int row_start, int j) {
+__device__ __forceinline__ int token_pos(const RowSpan& r, int row_start, int given) {
   if constexpr (kIds) {
-    const int id = __ldg(p.ids + (int64_t)t * p.ids_stride + j);
     // 64-bit: an id near the end of int32 minus a negative row start
-    const long long pos = (long long)id - row_start;
-    return id >= 0 && pos >= r.start && pos < r.end ? (int)pos : -1;
+    const long long pos = (long long)given - row_start;
+    return given >= 0 && pos >= r.start && pos < r.end ? (int)pos : -1;
   } else {
-    return r.start + j;
+    return r.start + given;
   }
 }
 
-// Looks the tokens of a warp's tiles up, a lane a token: the position of the
-// next tile to fetch and its page, and the position after it, are loaded two
-// tiles and one tile ahead of the copies that need them.
+// Looks the tokens of a warp's tiles up, a lane a token: pages two tiles ahead
+// of the copies that need them and ids, whose loads precede the pages', three,
+// so that the first copies wait for one id and one page only.
 template <bool kIds>
 struct Lookup {
   const AttentionParams& p;
-  const RowSpan r;
+  const RowSpan& r;
   const int32_t* table;
-  int t, row_start;
-  uint32_t j, step;  // n < 2^31: no overflow
-  int pos0, pos1, page0;
+  const int32_t* ids;
+  int row_start;
+  uint32_t j, step;        // n < 2^31: no overflow
+  int page0, page1;        // of the next tile to fetch and the one behind
+  int pos0, pos1, given2;  // ids only: their positions, and the id after that
 
   // tiles first, first + every, ... of row t
-  __device__ Lookup(const AttentionParams& p_, const RowSpan& r_, int t_, int first, int every)
-      : p(p_), r(r_), table(p_.table + (int64_t)r_.seq * p_.table_stride), t(t_) {
-    row_start = kIds && p.row_starts ? __ldg(p.row_starts + t) : 0;
+  __device__ Lookup(const AttentionParams& p_, const RowSpan& r_, int t, int first, int every)
+      : p(p_), r(r_), table(p_.table + (int64_t)r_.seq * p_.table_stride) {
     j = (uint32_t)kTile * (uint32_t)first + (threadIdx.x & 31);
     step = (uint32_t)kTile * (uint32_t)every;
-    pos0 = next();
-    pos1 = next();
-    page0 = page(pos0);
+    if constexpr (kIds) {
+      ids = p.ids + (int64_t)t * p.ids_stride;
+      row_start = p.row_starts ? __ldg(p.row_starts + t) : 0;
+      const int given0 = next(), given1 = next();
+      given2 = next();
+      pos0 = position(given0);
+      pos1 = position(given1);
+      page0 = page(pos0);
+      page1 = page(pos1);
+    } else {
+      page0 = page(place(j));
+      page1 = page(place(j + step));
+    }
   }
+  // The id at j, -1 beyond the last.  The ids' own number bounds their reads,
+  // so that these need not wait for the row's length.
   __device__ int next() {
-    const int pos = j < (uint32_t)r.n ? token_pos<kIds>(p, r, t, row_start, (int)j) : -1;
+    const int given = j < (uint32_t)p.num_ids ? __ldg(ids + j) : -1;
     j += step;
-    return pos;
+    return given;
   }
+  __device__ int position(int given) const {
+    return given < 0 ? -1 : token_pos<kIds>(r, row_start, given);
+  }
+  // A range's token at x, -1 beyond the last.
+  __device__ int place(uint32_t x) const { return x < (uint32_t)r.n ? r.start + (int)x : -1; }
   __device__ int page(int pos) const {
     return pos >= 0 ? __ldg(table + (pos >> p.c.page_shift)) : -1;
   }
   // Whether this lane's token of the current tile is in the cache, and its slot.
   __device__ bool slot(uint32_t& at) const {
     const bool ok = (uint32_t)page0 < p.c.num_pages;
-    at = ok ? ((uint32_t)page0 << p.c.page_shift) | (pos0 & ((1u << p.c.page_shift) - 1u)) : 0u;
+    const int pos = kIds ? pos0 : r.start + (int)j;
+    at = ok ? ((uint32_t)page0 << p.c.page_shift) | (pos & ((1u << p.c.page_shift) - 1u)) : 0u;
     return ok;
   }
   __device__ void advance() {
-    pos0 = pos1;
-    page0 = page(pos0);
-    pos1 = next();
+    page0 = page1;
+    if constexpr (kIds) {
+      pos0 = pos1;
+      pos1 = position(given2);
+      page1 = page(pos1);
+      given2 = next();
+    } else {
+      j += step;
+      page1 = page(place(j + step));
+    }
   }
 };
 
@@ -185,44 +211,48 @@ __device__ __forceinline__ constexpr int word_element(int tq, int w) {
   return D == 256 ? 128 * (w >> 2) + 32 * tq + 8 * (w & 3) : tq * (D / 4) + 8 * w;
 }
 
-// Head g's query values of this thread as the B operand of S^T = K Q^T,
-// with the scale's sign, scaled by a power of two so that the head's largest magnitude is in
-// [2^14, 2^15): bf16's 8 and fp16's 11 bits then fit fp16 for all elements
-// within 2^-28 of the largest.  Returns the power of two to undo.  Heads
-// beyond the group are zeros.
+// Head g's query values of this thread, as they are (pairs of 16-bit
+// elements); heads beyond the group are zeros.  Loaded before the first tokens
+// are looked up, converted after their copies have been sent off.
 template <int D>
-__device__ __forceinline__ float load_query(const AttentionParams& p, int t, int head, bool ok,
+__device__ __forceinline__ void fetch_query(const AttentionParams& p, int t, int head, bool ok,
                                             int tq, uint32_t (&qf)[D / 8]) {
-  float f[D / 4];
   const int64_t at = (int64_t)t * p.q_row_stride + (int64_t)head * p.q_head_stride;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q);
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {
     const int64_t from = at + word_element<D>(tq, w);
-    if (!ok) {
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (ok && p.q_vec) {
+      x = __ldg(reinterpret_cast<const uint4*>(q + from));
+    } else if (ok) {
+      uint32_t u[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[8 * w + e] = 0.0f;
-    } else if (p.q_vec) {
-      const uint4 x =
-          __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + from));
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (p.dtype == DCP_BF16) {
-          f[8 * w + 2 * e] = __uint_as_float(u[e] << 16);
-          f[8 * w + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-        } else {
-          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(u + e));
-          f[8 * w + 2 * e] = h.x, f[8 * w + 2 * e + 1] = h.y;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[8 * w + e] = load_element(p.q, from + e, p.dtype);
+      for (int e = 0; e < 4; ++e)
+        u[e] = __ldg(q + from + 2 * e) | ((uint32_t)__ldg(q + from + 2 * e + 1) << 16);
+      x = make_uint4(u[0], u[1], u[2], u[3]);
     }
+    qf[4 * w] = x.x, qf[4 * w + 1] = x.y, qf[4 * w + 2] = x.z, qf[4 * w + 3] = x.w;
   }
+}
+
+// These as the B operand of S^T = K Q^T, with the scale's sign, scaled by a
+// power of two so that the head's largest magnitude is in [2^14, 2^15): bf16's
+// 8 and fp16's 11 bits then fit fp16 for all elements within 2^-28 of the
+// largest.  Returns the power of two to undo.
+template <int D>
+__device__ __forceinline__ float convert_query(const AttentionParams& p, uint32_t (&qf)[D / 8]) {
+  auto pair = [&](uint32_t u) {
+    return p.dtype == DCP_BF16
+               ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u))
+               : __half22float2(*reinterpret_cast<const __half2*>(&u));
+  };
   float amax = 0.0f;
 #pragma unroll
-  for (int e = 0; e < D / 4; ++e) amax = fmaxf(amax, fabsf(f[e]));
+  for (int e = 0; e < D / 8; ++e) {
+    const float2 f = pair(qf[e]);
+    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   // exponent field of the largest magnitude; zero, subnormal and infinite
@@ -235,8 +265,10 @@ __device__ __forceinline__ float load_query(const AttentionParams& p, int t, int
       copysignf(__uint_as_float((uint32_t)(127 + shift / 2) << 23), p.scale);
   const float up2 = __uint_as_float((uint32_t)(127 + shift - shift / 2) << 23);
 #pragma unroll
-  for (int e = 0; e < D / 8; ++e)
-    qf[e] = pack_pair(f[2 * e] * up1 * up2, f[2 * e + 1] * up1 * up2, DCP_F16);
+  for (int e = 0; e < D / 8; ++e) {
+    const float2 f = pair(qf[e]);
+    qf[e] = pack_pair(f.x * up1 * up2, f.y * up1 * up2, DCP_F16);
+  }
   return __uint_as_float((uint32_t)(127 - shift / 2) << 23) *
          __uint_as_float((uint32_t)(127 - (shift - shift / 2)) << 23);
 }
@@ -256,14 +288,21 @@ struct Heads {
   float o[NT][kMTiles][4];
   float m[NT][2], l[NT][2];
 
-  __device__ void load(const AttentionParams& p, int t, int head0, int heads, bool write_mult) {
+  __device__ void fetch(const AttentionParams& p, int t, int head0, int heads) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      fetch_query<D>(p, t, head0 + 8 * n + g, 8 * n + g < heads, tq, qf[n]);
+  }
+
+  // What fetch() has loaded, made ready; sums from zero.
+  __device__ void begin(const AttentionParams& p, int t, int head0, int heads, bool write_mult) {
     const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const bool capped = p.softcap > 0.0f;
     const float unit = fabsf(capped ? p.scale / p.softcap : p.scale * kLog2e);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float undo =
-          load_query<D>(p, t, head0 + 8 * n + g, 8 * n + g < heads, tq, qf[n]) * unit;
+      const float undo = convert_query<D>(p, qf[n]) * unit;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         // above 0: -infinity times it stays -infinity
@@ -576,7 +615,8 @@ __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ At
     for (int i = 0; i < kMine; ++i) {
       const int64_t j = first + 32 * i;
       if (j >= n) continue;
-      const int pos = token_pos<kIds>(p, r, t, row_start, (int)j);
+      const int given = kIds ? __ldg(p.ids + (int64_t)t * p.ids_stride + j) : (int)j;
+      const int pos = token_pos<kIds>(r, row_start, given);
       if (pos >= 0 && pos < p.weights_width) {
         float* w = p.weights + (int64_t)t * p.weights_stride + pos;
         if constexpr (kIds)

@@ -8,9 +8,6 @@
 namespace dcp {
 namespace kv4 {
 
-constexpr int kWarps = 8;  // of a CTA
-constexpr int kThreads = 32 * kWarps;
-
 // Shared memory of one warp's stage: the tile's K and V code rows, its K and
 // V scales, the mask of present tokens.
 template <int D>
@@ -79,12 +76,13 @@ struct RingAt {
   }
 };
 
+// D * NT >= 256 takes up to 255 registers a thread, the others 128: 8 or 16
+// warps fit on an SM.
 template <int D, int NT>
 struct RingShape {
+  static constexpr int kWarpsPerSm = D * NT >= 256 ? 8 : 16;
   static constexpr int kStages = D == 256 ? 2 : 3;
-  static constexpr int kCtasPerSm = D * NT >= 256 ? 1 : 2;  // by registers
-  static constexpr int kRing = kStages * Stage<D>::kBytes;  // per warp
-  static constexpr int kSmem = kWarps * kRing;
+  static constexpr int kBytes = kStages * Stage<D>::kBytes;  // per warp
 };
 
 // One warp's tiles: every `of`-th of [tile0, tile1) of row t, from the
@@ -100,8 +98,9 @@ __device__ __forceinline__ void attend_tiles(const AttentionParams& p, const Row
   const int g = lane >> 2, tq = lane & 3;
   const int mine =
       tile1 - tile0 > sub ? (int)((unsigned)(tile1 - tile0 - sub + of - 1) / (unsigned)of) : 0;
-  uint8_t* ring = smem + warp * Shape::kRing;
+  uint8_t* ring = smem + warp * Shape::kBytes;
   const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
+  hd.fetch(p, t, head0, heads);
   Lookup<kIds> look(p, r, t, tile0 + sub, of);
 
   // Copies: chunk `chunk` of the rows row0 + i * kStep; the i-th row's
@@ -157,8 +156,7 @@ __device__ __forceinline__ void attend_tiles(const AttentionParams& p, const Row
 
 #pragma unroll
   for (int k = 0; k < Shape::kStages - 1; ++k) issue(k, k);
-  // Queries while the first tiles are under way.
-  hd.load(p, t, head0, heads, tile0 == 0 && sub == 0);
+  hd.begin(p, t, head0, heads, tile0 == 0 && sub == 0);
 
   uint32_t stage = 0, refill = Shape::kStages - 1;
   for (int k = 0; k < mine; ++k) {

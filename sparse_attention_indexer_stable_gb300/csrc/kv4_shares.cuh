@@ -4,7 +4,7 @@
 // the workspace, and a second kernel joins them.
 //
 // The key/value heads of a row are walked together, up to 8 at a time, by
-// 8 / together warps each: a token's rows of neighbouring heads are neighbours
+// kWarps / together warps each: a token's rows of neighbouring heads are neighbours
 // in memory, and DRAM serves 128 bytes at a time.  Walked one after the other,
 // 131072 tokens of 8 heads with 64-byte rows read 2.2 times their bytes.
 //
@@ -18,34 +18,54 @@
 namespace dcp {
 namespace kv4 {
 
+// 8 warps to a CTA.  One CTA of 16 warps per SM halves the number of pieces,
+// but nothing then runs while it drains: 259 us against 237 for 256 rows of up
+// to 8192 tokens.
+template <int D, int NT>
+struct ShareShape {
+  static constexpr int kWarps = 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kPerSm = RingShape<D, NT>::kWarpsPerSm / kWarps;
+  static constexpr int kSmem = kWarps * RingShape<D, NT>::kBytes;
+  // a warp's sums on their way to another: outputs, references, sums
+  static constexpr int kStateWords = NT * (D / 16 * 4 + 4);
+  static_assert(kWarps / 2 * kStateWords * 32 * 4 <= kSmem, "in the ring's place");
+};
+constexpr int kMostTogether = 8;  // key/value heads
+
 // The line of tiles: rows in order, in a row its units (groups of `together`
 // key/value heads, times head tiles), in a unit its tiles; a row that sees
 // nothing has one (empty) tile per unit, so that its outputs are written.
-// Share c is tiles [c * per, (c + 1) * per).
+// A unit's tiles are preceded by kPieceTiles places without one, for what its
+// beginning costs: its share is that much shorter.  Share c is the places
+// [c * per, (c + 1) * per).
 //
-// Record of a share, for the join: its last piece, if that is the first of a
-// unit that later shares go on with: x = row, y = unit, z = the last of those
-// shares (0: no such piece).
+// For the join, of a share: its last piece, if that is the first of a unit that
+// later shares go on with: x = row, y = unit, z = the last of those shares (0:
+// no such piece).  And of a unit, where there are few: its first and last share
+// (the same: nothing to join).
 struct Share {
-  int t, unit, tile0;  // where it begins
-  int left, per;       // its tiles, and those of a full share (host-checked: they fit)
+  int t, unit, at;  // where it begins
+  int left, per;    // its places, and those of a full share (host-checked: they fit)
 };
+constexpr int kPieceTiles = 2;
 
-__device__ __forceinline__ int tiles_of(const RowSpan& r) {
-  return max(1, (int)(((int64_t)r.n + kTile - 1) / kTile));
+__device__ __forceinline__ int places_of(const RowSpan& r) {
+  return kPieceTiles + max(1, (int)(((int64_t)r.n + kTile - 1) / kTile));
 }
 
-// This CTA's share, by prefix sums of the rows' tiles, each thread a run of
+// This CTA's share, by prefix sums of the rows' places, each thread a run of
 // rows.  Barriers: the whole CTA takes part.
-template <bool kIds>
+template <bool kIds, int kWarps>
 __device__ __forceinline__ Share find_share(const AttentionParams& p, int units, int of) {
   __shared__ long long warp_sum[kWarps];
   __shared__ Share share;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kThreads = 32 * kWarps;
   const int run = (p.rows + kThreads - 1) / kThreads;
   const int row0 = min(p.rows, (int)threadIdx.x * run), row1 = min(p.rows, row0 + run);
   long long own = 0;
-  for (int t = row0; t < row1; ++t) own += tiles_of(row_span<kIds>(p, t));
+  for (int t = row0; t < row1; ++t) own += places_of(row_span<kIds>(p, t));
   long long incl = own;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -62,12 +82,12 @@ __device__ __forceinline__ Share find_share(const AttentionParams& p, int units,
   }
   total *= units;
   // at least a tile for each of a head's warps
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)of);
+  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kPieceTiles + of));
   const long long x0 = min(total, blockIdx.x * per), x1 = min(total, x0 + per);
   if (x0 == x1 && threadIdx.x == 0) share = Share{0, 0, 0, 0, (int)per};
   if (x0 < x1 && before * units <= x0 && x0 < (before + own) * units) {
     for (int t = row0;; ++t) {
-      const int n = tiles_of(row_span<kIds>(p, t));
+      const int n = places_of(row_span<kIds>(p, t));
       if (x0 < (before + n) * units) {
         const int unit = (int)((x0 - before * units) / n);
         share = Share{t, unit, (int)(x0 - before * units - (long long)unit * n), (int)(x1 - x0),
@@ -82,25 +102,27 @@ __device__ __forceinline__ Share find_share(const AttentionParams& p, int units,
 }
 
 template <int D, int NT, bool kIds>
-__global__ void __launch_bounds__(kThreads, RingShape<D, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>::kPerSm)
     attention_shares_kernel(const __grid_constant__ AttentionParams p) {
-  constexpr int kMTiles = D / 16;
-  // a warp's sums on their way to another: outputs, references, sums
-  constexpr int kStateWords = NT * (kMTiles * 4 + 4);
-  static_assert(kWarps / 2 * kStateWords * 32 * 4 <= RingShape<D, NT>::kSmem, "fits the ring");
+  using Shape = ShareShape<D, NT>;
+  constexpr int kMTiles = D / 16, kStateWords = Shape::kStateWords;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
   const int groups = (p.c.heads + p.together - 1) / p.together;
-  const int of = kWarps / p.together;           // warps of a head
+  const int of = Shape::kWarps / p.together;    // warps of a head
   const int head = warp / of, sub = warp % of;  // this warp's head of the group, its turn
   grid_dependency_wait();
-  Share s = find_share<kIds>(p, groups * p.head_tiles, of);
+  Share s = find_share<kIds, Shape::kWarps>(p, groups * p.head_tiles, of);
 
   int4 record = make_int4(0, 0, 0, 0);
   while (s.left > 0) {
     const RowSpan r = row_span<kIds>(p, s.t);
-    const int tiles = tiles_of(r), tile0 = s.tile0, tile1 = min(tiles - tile0, s.left) + tile0;
+    // this share's places of the unit: [s.at, to), tile i at kPieceTiles + i
+    const int places = places_of(r), to = min(places - s.at, s.left) + s.at;
+    const int tiles = places - kPieceTiles;
+    const int tile0 = max(0, s.at - kPieceTiles), tile1 = max(0, to - kPieceTiles);
+    if (tile1 == tile0) break;  // the share's end, and not a tile of the unit
     const int h = s.unit % groups * p.together + head, ht = s.unit / groups;
     const bool active = h < p.c.heads;
     const int heads = active ? min(8 * NT, p.group - ht * 8 * NT) : 0;  // query heads
@@ -153,8 +175,12 @@ __global__ void __launch_bounds__(kThreads, RingShape<D, NT>::kCtasPerSm)
     }
 
     const bool whole = tile0 == 0 && tile1 == tiles;
-    if (!whole && tile0 == 0)
-      record = make_int4(s.t, s.unit, (int)blockIdx.x + (tiles - tile1 + s.per - 1) / s.per, 0);
+    if (tile0 == 0) {
+      const int last = (int)blockIdx.x + (places - to + s.per - 1) / s.per;
+      if (!whole) record = make_int4(s.t, s.unit, last, 0);
+      if (p.cuts && threadIdx.x == 0)
+        p.cuts[(int64_t)s.t * groups * p.head_tiles + s.unit] = make_int2((int)blockIdx.x, last);
+    }
     if (sub == 0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -192,92 +218,104 @@ __global__ void __launch_bounds__(kThreads, RingShape<D, NT>::kCtasPerSm)
           }
         }
     }
-    s.left -= tile1 - tile0;
-    s.tile0 = 0;
+    s.left -= to - s.at;
+    s.at = 0;
     if (++s.unit == groups * p.head_tiles) s.unit = 0, ++s.t;
   }
   if (threadIdx.x == 0) p.shares[blockIdx.x] = record;
 }
 
 // Joins the pieces of a unit that shares cut.  kByUnit: a CTA per unit and
-// query head (few units of many pieces), its warps dealt the pieces; the
-// unit's first share is found among the records.  Otherwise a CTA per share
-// (for the unit whose first piece is the share's last) and 8 query heads, a
-// warp each.  A lane holds D / 32 contiguous elements.
+// query head (few units of many pieces), its warps dealt the pieces.  Otherwise
+// a CTA per share (for the unit whose first piece is the share's last) and 8
+// query heads, a warp each.  A lane holds D / 32 contiguous elements.
 constexpr int kJoinWarps = 8;
 
 template <int D, int NT, bool kByUnit>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-    join_shares_kernel(const __grid_constant__ AttentionParams p, int shares) {
+    join_shares_kernel(const __grid_constant__ AttentionParams p) {
   constexpr int kPer = D / 32;
   constexpr int kWays = kByUnit ? kJoinWarps : 1;
-  __shared__ float red[kByUnit ? kJoinWarps : 1][D];
-  __shared__ float red_l[kJoinWarps];
-  __shared__ int s_share;
-  __shared__ int4 s_record;
+  __shared__ float red[kWays][D];
+  __shared__ float2 red_ml[kWays];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (p.c.heads + p.together - 1) / p.together;
-  grid_dependency_wait();
-  int c = blockIdx.x;
-  if constexpr (kByUnit) {
-    const int units = groups * p.head_tiles;
-    if (threadIdx.x == 0) s_share = -1;
-    __syncthreads();
-    for (int i = threadIdx.x; i < shares; i += 32 * kJoinWarps) {
-      const int4 x = p.shares[i];
-      if (x.z && x.x == (int)blockIdx.x / units && x.y == (int)blockIdx.x % units) {
-        s_share = i;
-        s_record = x;
-      }
-    }
-    __syncthreads();
-    c = s_share;
-    if (c < 0) return;  // one share walked the whole unit
-  }
-  const int4 record = kByUnit ? s_record : p.shares[c];
-  if (!record.z) return;
+  const int units = groups * p.head_tiles;
   const int q = kByUnit ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
   const int kv = q / (8 * NT), head = q % (8 * NT);
-  const int h = record.y % groups * p.together + kv, ht = record.y / groups;
+  grid_dependency_wait();
+  int t, unit, c, last;
+  if constexpr (kByUnit) {
+    const int2 cut = p.cuts[blockIdx.x];
+    t = blockIdx.x / units, unit = blockIdx.x % units;
+    c = cut.x, last = cut.y;
+  } else {
+    const int4 record = p.shares[blockIdx.x];
+    t = record.x, unit = record.y;
+    c = blockIdx.x, last = max(c, record.z);
+  }
+  if (last == c) return;  // one share walked the whole unit
+  const int h = unit % groups * p.together + kv, ht = unit / groups;
   // the whole CTA with kByUnit, else this warp (no barrier follows)
   if (ht * 8 * NT + head >= p.group || h >= p.c.heads) return;
-  const int last = record.z;
   auto piece = [&](int i) {
     return (((int64_t)2 * i + (i == c)) * p.together + kv) * 8 * NT + head;
   };
+  // this warp's pieces, the references of up to 32 at a time in its lanes
   Joined j{kNoScore, 0.0f, 0.0f, 0.0f};
-  for (int i = c + lane; i <= last; i += 32) j.top = fmaxf(j.top, p.part_ml[piece(i)].x);
-#pragma unroll
-  for (int x = 16; x; x >>= 1) j.top = fmaxf(j.top, __shfl_xor_sync(0xffffffffu, j.top, x));
   float acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
-#pragma unroll 8
-  for (int i = c + (kByUnit ? warp : 0); i <= last; i += kWays) {
-    const int64_t at = piece(i);
-    const float2 v = p.part_ml[at];
-    const float f = exp2_approx(v.x - j.top);
-    const float* src = p.part_out + at * D + lane * kPer;
-    j.sum += f * v.y;
+  for (int i0 = c + (kByUnit ? warp : 0); i0 <= last; i0 += 32 * kWays) {
+    const int mine = i0 + lane * kWays;
+    const float2 ml = mine <= last ? p.part_ml[piece(mine)] : make_float2(kNoScore, 0.0f);
+    float top = ml.x;
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2) {
-      const float2 w = *reinterpret_cast<const float2*>(src + e);
-      acc[e] += f * w.x;
-      acc[e + 1] += f * w.y;
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    top = fmaxf(top, j.top);
+    const float scale = exp2_approx(j.top - top), f = exp2_approx(ml.x - top);
+    j.top = top;
+    j.sum = j.sum * scale + f * ml.y;  // of this lane's pieces
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= scale;
+    const int count = min(32, (last - i0) / kWays + 1);
+#pragma unroll 8
+    for (int k = 0; k < count; ++k) {
+      const float* src = p.part_out + piece(i0 + k * kWays) * D + lane * kPer;
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      if constexpr (kPer == 2) {
+        const float2 w = *reinterpret_cast<const float2*>(src);
+        acc[0] += fk * w.x, acc[1] += fk * w.y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer; e += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(src + e);
+          acc[e] += fk * w.x, acc[e + 1] += fk * w.y;
+          acc[e + 2] += fk * w.z, acc[e + 3] += fk * w.w;
+        }
+      }
     }
   }
-  const int64_t at = (int64_t)record.x * p.q_heads + h * p.group + ht * 8 * NT + head;
+#pragma unroll
+  for (int x = 16; x; x >>= 1) j.sum += __shfl_xor_sync(0xffffffffu, j.sum, x);
+  const int64_t at = (int64_t)t * p.q_heads + h * p.group + ht * 8 * NT + head;
   if constexpr (kByUnit) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) red[warp][lane * kPer + e] = acc[e];
-    if (lane == 0) red_l[warp] = j.sum;
+    if (lane == 0) red_ml[warp] = make_float2(j.top, j.sum);
     __syncthreads();
-    j.sum = 0.0f;
+    j = Joined{kNoScore, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) j.sum += red_l[w];
+    for (int w = 0; w < kWays; ++w) j.top = fmaxf(j.top, red_ml[w].x);
     for (int d = 2 * threadIdx.x; d < D; d += 64 * kJoinWarps) {
+      j.sum = j.x = j.y = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) j.x += red[w][d], j.y += red[w][d + 1];
+      for (int w = 0; w < kWays; ++w) {
+        const float f = exp2_approx(red_ml[w].x - j.top);
+        j.sum += f * red_ml[w].y;
+        j.x += f * red[w][d];
+        j.y += f * red[w][d + 1];
+      }
       write_out<D>(p, at, d, j);
     }
   } else {

@@ -9,14 +9,17 @@
 namespace dcp {
 namespace kv4 {
 
+constexpr int kSliceWarps = 8;
+constexpr int kSliceThreads = 32 * kSliceWarps;
+
 // The join, in the ring's place: each warp's outputs (padded rows), references
 // and sums, and behind them the CTA's own for the cluster (16 bytes per output
 // pair).
 template <int D, int NT>
 struct SliceJoin {
   static constexpr int kStride = D + 4;
-  static constexpr int kWarpBytes = (kWarps * 8 * NT * (kStride + 2) * 4 + 15) & ~15;
-  static_assert(kWarpBytes + 8 * NT * D / 2 * 16 <= RingShape<D, NT>::kSmem, "fits the ring");
+  static constexpr int kWarpBytes = (kSliceWarps * 8 * NT * (kStride + 2) * 4 + 15) & ~15;
+  static_assert(kWarpBytes + 8 * NT * D / 2 * 16 <= kSliceWarps * RingShape<D, NT>::kBytes, "fits the ring");
 };
 
 // Leaves a warp's sums in shared memory (all warps of the CTA: barriers).
@@ -27,8 +30,8 @@ __device__ __forceinline__ void leave_sums(const Heads<D, NT>& hd, uint8_t* smem
   const int g = lane >> 2, tq = lane & 3;
   __syncthreads();  // every warp has read its ring
   float* join_o = reinterpret_cast<float*>(smem);
-  float* join_m = join_o + kWarps * 8 * NT * Join::kStride;
-  float* join_l = join_m + kWarps * 8 * NT;
+  float* join_m = join_o + kSliceWarps * 8 * NT * Join::kStride;
+  float* join_l = join_m + kSliceWarps * 8 * NT;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -53,13 +56,13 @@ template <int D, int NT>
 __device__ __forceinline__ Joined join_warps(const uint8_t* smem, int head, int d) {
   using Join = SliceJoin<D, NT>;
   const float* join_o = reinterpret_cast<const float*>(smem);
-  const float* join_m = join_o + kWarps * 8 * NT * Join::kStride;
-  const float* join_l = join_m + kWarps * 8 * NT;
+  const float* join_m = join_o + kSliceWarps * 8 * NT * Join::kStride;
+  const float* join_l = join_m + kSliceWarps * 8 * NT;
   Joined j{kNoScore, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) j.top = fmaxf(j.top, join_m[w * 8 * NT + head]);
+  for (int w = 0; w < kSliceWarps; ++w) j.top = fmaxf(j.top, join_m[w * 8 * NT + head]);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kSliceWarps; ++w) {
     const int col = w * 8 * NT + head;
     const float f = exp2_approx(join_m[col] - j.top);
     const float2 v = *reinterpret_cast<const float2*>(join_o + col * Join::kStride + d);
@@ -72,7 +75,7 @@ __device__ __forceinline__ Joined join_warps(const uint8_t* smem, int head, int 
 
 // blockIdx.x = ((row * head_tiles + head tile) * heads + head) * slices + slice.
 template <int D, int NT, bool kIds>
-__global__ void __launch_bounds__(kThreads, RingShape<D, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(kSliceThreads, RingShape<D, NT>::kWarpsPerSm / kSliceWarps)
     attention_slices_kernel(const __grid_constant__ AttentionParams p) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -92,13 +95,13 @@ __global__ void __launch_bounds__(kThreads, RingShape<D, NT>::kCtasPerSm)
   const int per = (tiles + slices - 1) / slices;
   const int tile0 = min(tiles, slice * per), tile1 = min(tiles, tile0 + per);
   Heads<D, NT> hd;
-  attend_tiles<D, NT, kIds>(p, r, t, h, head0, heads, tile0, tile1, threadIdx.x >> 5, kWarps,
+  attend_tiles<D, NT, kIds>(p, r, t, h, head0, heads, tile0, tile1, threadIdx.x >> 5, kSliceWarps,
                             smem, hd);
   leave_sums<D, NT>(hd, smem);
 
   const int64_t at = (int64_t)t * p.q_heads + head0;
   if (slices == 1) {
-    for (int i = threadIdx.x; i < heads * (D / 2); i += kThreads) {
+    for (int i = threadIdx.x; i < heads * (D / 2); i += kSliceThreads) {
       const int head = i / (D / 2), d = 2 * (i % (D / 2));
       write_out<D>(p, at + head, d, join_warps<D, NT>(smem, head, d));
     }
@@ -107,11 +110,11 @@ __global__ void __launch_bounds__(kThreads, RingShape<D, NT>::kCtasPerSm)
   // The CTA's own join goes behind the warps' (each thread its own values),
   // then every CTA adds its part of the outputs over the cluster.
   Joined* mine = reinterpret_cast<Joined*>(smem + SliceJoin<D, NT>::kWarpBytes);
-  for (int i = threadIdx.x; i < heads * (D / 2); i += kThreads)
+  for (int i = threadIdx.x; i < heads * (D / 2); i += kSliceThreads)
     mine[i] = join_warps<D, NT>(smem, i / (D / 2), 2 * (i % (D / 2)));
   cluster.sync();
-  for (int i = slice * kThreads + threadIdx.x; i < heads * (D / 2);
-       i += slices * kThreads) {
+  for (int i = slice * kSliceThreads + threadIdx.x; i < heads * (D / 2);
+       i += slices * kSliceThreads) {
     Joined j{kNoScore, 0.0f, 0.0f, 0.0f};
     Joined other[8];
 #pragma unroll

@@ -82,7 +82,8 @@ template <int D, int NT>
 struct RingShape {
   static constexpr int kWarpsPerSm = D * NT >= 256 ? 8 : 16;
   static constexpr int kStages = D == 256 ? 2 : 3;
-  static constexpr int kBytes = kStages * Stage<D>::kBytes;  // per warp
+  static constexpr int kQueue = kStages * Stage<D>::kBytes;  // ids on their way
+  static constexpr int kBytes = kQueue + kIdQueue * 32 * 4;  // per warp
 };
 
 // One warp's tiles: every `of`-th of [tile0, tile1) of row t, from the
@@ -101,7 +102,7 @@ __device__ __forceinline__ void attend_tiles(const AttentionParams& p, const Row
   uint8_t* ring = smem + warp * Shape::kBytes;
   const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
   hd.fetch(p, t, head0, heads);
-  Lookup<kIds> look(p, r, t, tile0 + sub, of);
+  Lookup<kIds> look(p, r, t, tile0 + sub, of, ring + Shape::kQueue);
 
   // Copies: chunk `chunk` of the rows row0 + i * kStep; the i-th row's
   // destination lies at a constant distance (at dim 256 with a flipped chunk).
@@ -149,7 +150,7 @@ __device__ __forceinline__ void attend_tiles(const AttentionParams& p, const Row
                             ok);
       }
       if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::kBytes + S::kMask) = mask;
-      look.advance();
+      look.advance(k);
     }
     cp_async_commit();
   };

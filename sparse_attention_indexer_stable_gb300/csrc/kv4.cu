@@ -132,7 +132,8 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   plan->heads_per_cta = group > 8 && c->dim <= 128 ? 16 : 8;
   plan->head_tiles = (group + plan->heads_per_cta - 1) / plan->heads_per_cta;
   // Slices or shares, whichever has fewer tiles on its longest warp.  Lengths
-  // are on the device: both are judged at the longest row.
+  // are on the device: slices, as long as the longest row, are judged by that,
+  // shares by three quarters of it where rows may differ.
   const int64_t units = (int64_t)a->rows * c->heads * plan->head_tiles;
   const int64_t tiles = ((int64_t)plan->width + kTile - 1) / kTile;
   const int64_t warps = c->dim * plan->heads_per_cta >= 2048 ? 8 : 16;  // of an SM
@@ -149,7 +150,8 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
     plan->together /= 2;
   const int64_t padded = units / c->heads * ceil_div(c->heads, plan->together) * plan->together;
   plan->shares = 0;
-  if (ceil_div(padded * tiles, kPlanSms * warps) + kPieceCost + kShareCost < least) {
+  const int64_t mean = a->ids || a->rows == 1 ? tiles : tiles * 3 / 4;
+  if (ceil_div(padded * mean, kPlanSms * warps) + kPieceCost + kShareCost < least) {
     plan->slices = 0;
     plan->shares = (int)(kPlanSms * warps / kSliceWarps);  // as many CTAs of 8 warps as fit
   }
@@ -249,7 +251,7 @@ static dcp_status store_args(const dcp_kv4_cache* cache, const void* k, const vo
 }
 
 static dim3 store_grid(const StoreParams& p) {
-  return dim3((unsigned)((p.N * p.c.heads * p.blocks + 255) / 256), 2);
+  return dim3((unsigned)((p.N * p.c.heads * p.blocks + 255) / 256));
 }
 
 dcp_status dcp_kv4_append(const dcp_kv4_cache* cache, const void* k, const void* v, int dtype,

@@ -1,9 +1,9 @@
 // kv4_store.cuh -- writing tokens into the 4-bit cache and reading them back.
 //
-// One thread per block of 16 elements: a block's amax, scale and codes need
-// nothing from other threads, its loads are 32 or 64 contiguous bytes and
-// neighbouring threads take neighbouring blocks, so both sides are coalesced.
-// Bound by memory: 2.56 bytes move per 16-bit element.
+// One thread per block of 16 elements, of K and of V: a block's amax, scale and
+// codes need nothing from other threads, its loads are 32 or 64 contiguous
+// bytes and neighbouring threads take neighbouring blocks, so both sides are
+// coalesced.  2.56 bytes move per 16-bit element.
 #pragma once
 
 #include "kv4_common.cuh"
@@ -23,32 +23,49 @@ struct StoreParams {
   int blocks;  // per head: dim / 16
 };
 
-// A block of 16 elements (i: its first, in elements of dtype): its values in
-// fp32 and their largest magnitude, NaN if any element is NaN.
-__device__ __forceinline__ float load_block(const void* base, int64_t i, int dtype, bool vec,
-                                            float (&x)[16]) {
-  if (dtype == DCP_F32 || !vec) {
-    if (vec) {
-      const float* p = static_cast<const float*>(base) + i;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p) + e);
-        x[4 * e] = v.x, x[4 * e + 1] = v.y, x[4 * e + 2] = v.z, x[4 * e + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = load_element(base, i + e, dtype);
-    }
-    float amax = 0.0f;
+// A block of 16 elements as it lies in memory: 32 bytes, or 64 of fp32.
+struct RawBlock {
+  uint4 v[4];
+};
+
+__device__ __forceinline__ RawBlock load_block(const void* base, int64_t i, int dtype, bool vec) {
+  RawBlock r;
+  if (vec) {
+    const uint4* p = dtype == DCP_F32
+                         ? reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i)
+                         : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+    r.v[0] = __ldg(p);
+    r.v[1] = __ldg(p + 1);
+    if (dtype == DCP_F32) r.v[2] = __ldg(p + 2), r.v[3] = __ldg(p + 3);
+    return r;
+  }
+  uint32_t* w = reinterpret_cast<uint32_t*>(r.v);
+  if (dtype == DCP_F32) {
 #pragma unroll
     for (int e = 0; e < 16; ++e)
+      w[e] = __float_as_uint(__ldg(static_cast<const float*>(base) + i + e));
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + i;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      w[e] = __ldg(p + 2 * e) | ((uint32_t)__ldg(p + 2 * e + 1) << 16);
+  }
+  return r;
+}
+
+// Its values in fp32 and their largest magnitude, NaN if any element is NaN.
+__device__ __forceinline__ float unpack_block(const RawBlock& r, int dtype, float (&x)[16]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
+  if (dtype == DCP_F32) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      x[e] = __uint_as_float(w[e]);
       asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(x[e])));
+    }
     return amax;
   }
   // pairs of 16-bit elements: magnitudes compared two at a time
-  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-  const uint4 v[2] = {__ldg(p), __ldg(p + 1)};
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
   uint32_t top = 0u;
   if (dtype == DCP_BF16) {
 #pragma unroll
@@ -156,41 +173,33 @@ __device__ __forceinline__ bool find_block(const StoreParams& p, int64_t& n, int
 
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ StoreParams p) {
   grid_dependency_wait();
-  const int which = blockIdx.y;  // 0: K, 1: V
   int64_t n;
   int r;
   if (!find_block(p, n, r)) return;
-  const int64_t per_token = (int64_t)p.c.heads * p.blocks;
   const int h = r / p.blocks, b = r - h * p.blocks;
   const int64_t slot = __ldg(p.slots + n);
+  RawBlock raw[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)  // K, V
+    raw[i] = load_block(p.in[i], n * p.row_stride[i] + h * p.head_stride[i] + b * kBlock, p.dtype,
+                        p.vec[i]);
   if ((uint64_t)slot >= p.c.num_slots()) return;
-  float x[16];
-  const float amax = load_block(p.in[which], n * p.row_stride[which] + h * p.head_stride[which] + b * kBlock,
-                                p.dtype, p.vec[which], x);
-  uint8_t scale;
-  const uint2 codes =
-      encode_block(x, amax, 1.0f / (which ? p.c.v_unit : p.c.k_unit), p.dtype != DCP_F32, scale);
-  const int64_t at = slot * per_token + r;  // block's index in the plane
-  reinterpret_cast<uint2*>(which ? p.c.v_codes : p.c.k_codes)[at] = codes;
-  (which ? p.c.v_scales : p.c.k_scales)[at] = scale;
+  const int64_t at = slot * (p.c.heads * p.blocks) + r;  // block's index in the plane
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float x[16];
+    const float amax = unpack_block(raw[i], p.dtype, x);
+    uint8_t scale;
+    const uint2 codes = encode_block(x, amax, 1.0f / (i ? p.c.v_unit : p.c.k_unit),
+                                     p.dtype != DCP_F32, scale);
+    reinterpret_cast<uint2*>(i ? p.c.v_codes : p.c.k_codes)[at] = codes;
+    (i ? p.c.v_scales : p.c.k_scales)[at] = scale;
+  }
 }
 
-__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ StoreParams p) {
-  grid_dependency_wait();
-  const int which = blockIdx.y;
-  int64_t n;
-  int r;
-  if (!find_block(p, n, r)) return;
-  const int64_t per_token = (int64_t)p.c.heads * p.blocks, i = n * per_token + r;
-  const int64_t slot = __ldg(p.slots + n);
-  uint2 codes = make_uint2(0u, 0u);
-  uint32_t scale = 0u;
-  if ((uint64_t)slot < p.c.num_slots()) {
-    const int64_t at = slot * per_token + r;
-    codes = __ldg(reinterpret_cast<const uint2*>(which ? p.c.v_codes : p.c.k_codes) + at);
-    scale = __ldg((which ? p.c.v_scales : p.c.k_scales) + at);
-  }
-  const float unit = which ? p.c.v_unit : p.c.k_unit;
+// The values of a block in fp32.
+__device__ __forceinline__ void decode_block(uint2 codes, uint32_t scale, float unit,
+                                             float2 (&f)[8]) {
   const uint32_t s2 = scales_to_half(scale | (scale << 8));
   uint32_t d[8], w[4];
   codes_to_half(codes.x, w);
@@ -199,24 +208,46 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ Store
   codes_to_half(codes.y, w);
 #pragma unroll
   for (int e = 0; e < 4; ++e) d[4 + e] = hmul2(w[e], s2);
-  float2 f[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     f[e] = __half22float2(*reinterpret_cast<const __half2*>(d + e));
     f[e].x *= unit, f[e].y *= unit;
   }
-  if (p.dtype == DCP_F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out[which]) + i * kBlock);
+}
+
+__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ StoreParams p) {
+  grid_dependency_wait();
+  int64_t n;
+  int r;
+  if (!find_block(p, n, r)) return;
+  const int64_t per_token = (int64_t)p.c.heads * p.blocks, i = n * per_token + r;
+  const int64_t slot = __ldg(p.slots + n);
+  uint2 codes[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};  // K, V
+  uint32_t scale[2] = {0u, 0u};
+  if ((uint64_t)slot < p.c.num_slots()) {
+    const int64_t at = slot * per_token + r;
+    codes[0] = __ldg(reinterpret_cast<const uint2*>(p.c.k_codes) + at);
+    codes[1] = __ldg(reinterpret_cast<const uint2*>(p.c.v_codes) + at);
+    scale[0] = __ldg(p.c.k_scales + at);
+    scale[1] = __ldg(p.c.v_scales + at);
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o[e] = make_float4(f[2 * e].x, f[2 * e].y, f[2 * e + 1].x, f[2 * e + 1].y);
-  } else {
-    uint32_t u[8];
+  for (int k = 0; k < 2; ++k) {
+    float2 f[8];
+    decode_block(codes[k], scale[k], k ? p.c.v_unit : p.c.k_unit, f);
+    if (p.dtype == DCP_F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out[k]) + i * kBlock);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] = pack_pair(f[e].x, f[e].y, p.dtype);
-    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[which]) + i * kBlock);
-    o[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    o[1] = make_uint4(u[4], u[5], u[6], u[7]);
+      for (int e = 0; e < 4; ++e)
+        o[e] = make_float4(f[2 * e].x, f[2 * e].y, f[2 * e + 1].x, f[2 * e + 1].y);
+    } else {
+      uint32_t u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = pack_pair(f[e].x, f[e].y, p.dtype);
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[k]) + i * kBlock);
+      o[0] = make_uint4(u[0], u[1], u[2], u[3]);
+      o[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
   }
 }
 

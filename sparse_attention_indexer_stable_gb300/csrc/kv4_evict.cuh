@@ -275,20 +275,27 @@ __global__ void __launch_bounds__(kSelThreads, 1)
 
 constexpr int kCopy = 4;  // tokens of a warp
 
-// Rows of one plane (those that are live), all loads before the stores.
+// Rows of the K and V planes of one kind (those that are live), all loads
+// before the stores.
 template <typename Piece>
-__device__ __forceinline__ void copy_rows(uint8_t* plane, const uint64_t (&dst)[kCopy],
+__device__ __forceinline__ void copy_rows(uint8_t* k_plane, uint8_t* v_plane,
+                                          const uint64_t (&dst)[kCopy],
                                           const uint64_t (&src)[kCopy], unsigned live, int bytes,
                                           int lane) {
   for (int i = lane; i < bytes / (int)sizeof(Piece); i += 32) {
-    Piece x[kCopy];
+    Piece x[kCopy], y[kCopy];
 #pragma unroll
     for (int k = 0; k < kCopy; ++k)
-      if ((live >> k) & 1u)
-        x[k] = reinterpret_cast<const Piece*>(plane + src[k] * (uint64_t)bytes)[i];
+      if ((live >> k) & 1u) {
+        x[k] = reinterpret_cast<const Piece*>(k_plane + src[k] * (uint64_t)bytes)[i];
+        y[k] = reinterpret_cast<const Piece*>(v_plane + src[k] * (uint64_t)bytes)[i];
+      }
 #pragma unroll
     for (int k = 0; k < kCopy; ++k)
-      if ((live >> k) & 1u) reinterpret_cast<Piece*>(plane + dst[k] * (uint64_t)bytes)[i] = x[k];
+      if ((live >> k) & 1u) {
+        reinterpret_cast<Piece*>(k_plane + dst[k] * (uint64_t)bytes)[i] = x[k];
+        reinterpret_cast<Piece*>(v_plane + dst[k] * (uint64_t)bytes)[i] = y[k];
+      }
   }
 }
 
@@ -322,10 +329,8 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
     src[k] = __shfl_sync(0xffffffffu, from, k);
     dst[k] = __shfl_sync(0xffffffffu, to, k);
   }
-  copy_rows<uint4>(p.c.k_codes, dst, src, live, p.row_codes, lane);
-  copy_rows<uint4>(p.c.v_codes, dst, src, live, p.row_codes, lane);
-  copy_rows<uint32_t>(p.c.k_scales, dst, src, live, p.row_scales, lane);
-  copy_rows<uint32_t>(p.c.v_scales, dst, src, live, p.row_scales, lane);
+  copy_rows<uint32_t>(p.c.k_scales, p.c.v_scales, dst, src, live, p.row_scales, lane);
+  copy_rows<uint4>(p.c.k_codes, p.c.v_codes, dst, src, live, p.row_codes, lane);
 }
 
 }  // namespace kv4

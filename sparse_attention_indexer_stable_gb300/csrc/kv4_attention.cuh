@@ -126,15 +126,14 @@ struct Lookup {
   int page0, page1;    // of the next tile to fetch and the one behind
   int pos0, pos1;      // ids only: their positions
 
-  // tiles first, first + every, ... of row t
+  // tiles first, first + every, ... of row t; of each the token `token`
   __device__ Lookup(const AttentionParams& p_, const RowSpan& r_, int t, int first, int every,
-                    uint8_t* queue_)
+                    int token, uint8_t* queue_)
       : p(p_), r(r_), table(p_.table + (int64_t)r_.seq * p_.table_stride) {
-    const int lane = threadIdx.x & 31;
-    j = (uint32_t)kTile * (uint32_t)first + lane;
+    j = (uint32_t)kTile * (uint32_t)first + token;
     step = (uint32_t)kTile * (uint32_t)every;
     if constexpr (kIds) {
-      queue = reinterpret_cast<int32_t*>(queue_) + lane;
+      queue = reinterpret_cast<int32_t*>(queue_) + (threadIdx.x & 31);
       ids = p.ids + (int64_t)t * p.ids_stride;
       row_start = p.row_starts ? __ldg(p.row_starts + t) : 0;
       int given[5];  // tiles 0 to 4: their own number bounds the reads, not the row's length

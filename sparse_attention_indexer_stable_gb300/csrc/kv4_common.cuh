@@ -116,6 +116,12 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool ok)
                  : "memory");
 }
 
+// 16 bytes of which the last may be zeros: `bytes` (0 to 16) are read.
+__device__ __forceinline__ void cp_async_some(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
 // The same without the choice.
 template <int N>
 __device__ __forceinline__ void cp_async_all(uint32_t dst, const void* src) {

@@ -102,7 +102,7 @@ __device__ __forceinline__ void attend_tiles(const AttentionParams& p, const Row
   uint8_t* ring = smem + warp * Shape::kBytes;
   const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
   hd.fetch(p, t, head0, heads);
-  Lookup<kIds> look(p, r, t, tile0 + sub, of, ring + Shape::kQueue);
+  Lookup<kIds> look(p, r, t, tile0 + sub, of, lane, ring + Shape::kQueue);
 
   // Copies: chunk `chunk` of the rows row0 + i * kStep; the i-th row's
   // destination lies at a constant distance (at dim 256 with a flipped chunk).

@@ -13,7 +13,7 @@
 // against 271 us for 256 rows of up to 8192 tokens.
 #pragma once
 
-#include "kv4_ring.cuh"
+#include "kv4_team.cuh"
 
 namespace dcp {
 namespace kv4 {
@@ -26,7 +26,10 @@ struct ShareShape {
   static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPerSm = RingShape<D, NT>::kWarpsPerSm / kWarps;
-  static constexpr int kSmem = kWarps * RingShape<D, NT>::kBytes;
+  static constexpr int kTeam = TeamStage<D>::kTeam;
+  static constexpr int kRings = kWarps * RingShape<D, NT>::kBytes;
+  static constexpr int kTeams = kWarps / kTeam * TeamShape<D, NT>::kBytes;
+  static constexpr int kSmem = D < 256 && kTeams > kRings ? kTeams : kRings;
   // a warp's sums on their way to another: outputs, references, sums
   static constexpr int kStateWords = NT * (D / 16 * 4 + 4);
   static_assert(kWarps / 2 * kStateWords * 32 * 4 <= kSmem, "in the ring's place");
@@ -101,7 +104,7 @@ __device__ __forceinline__ Share find_share(const AttentionParams& p, int units,
   return share;
 }
 
-template <int D, int NT, bool kIds>
+template <int D, int NT, bool kIds, bool kTeam>
 __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>::kPerSm)
     attention_shares_kernel(const __grid_constant__ AttentionParams p) {
   using Shape = ShareShape<D, NT>;
@@ -110,8 +113,12 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
   const int groups = (p.c.heads + p.together - 1) / p.together;
-  const int of = Shape::kWarps / p.together;    // warps of a head
-  const int head = warp / of, sub = warp % of;  // this warp's head of the group, its turn
+  const int of = Shape::kWarps / p.together;  // warps of a head
+  // this warp's head of the group and its turn; the warps of a team have
+  // neighbouring heads and the same turn
+  constexpr int kMembers = kTeam ? Shape::kTeam : 1;
+  const int rest = warp / kMembers;
+  const int head = rest / of * kMembers + warp % kMembers, sub = rest % of;
   grid_dependency_wait();
   Share s = find_share<kIds, Shape::kWarps>(p, groups * p.head_tiles, of);
 
@@ -128,8 +135,13 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
     const int heads = active ? min(8 * NT, p.group - ht * 8 * NT) : 0;  // query heads
     const int head0 = h * p.group + ht * 8 * NT;
     Heads<D, NT> hd;
-    attend_tiles<D, NT, kIds>(p, r, s.t, active ? h : 0, head0, heads, tile0,
-                              active ? tile1 : tile0, sub, of, smem, hd);
+    if constexpr (kTeam)
+      attend_team<D, NT, kIds>(p, r, s.t, h - warp % kMembers,
+                               min(kMembers, p.c.heads - (h - warp % kMembers)), warp % kMembers,
+                               active, head0, heads, tile0, tile1, sub, of, smem, hd);
+    else
+      attend_tiles<D, NT, kIds>(p, r, s.t, active ? h : 0, head0, heads, tile0,
+                                active ? tile1 : tile0, sub, of, smem, hd);
 
     // the warps of a head add up in halves, in the ring's place
     float* state = reinterpret_cast<float*>(smem);

@@ -254,6 +254,39 @@ def test_even_shares_over_many_rows_of_all_lengths(dk):
     check(dk, cache, host, q[few], values[few], "f16", table[few], lens[few], ids=ids)
 
 
+@pytest.mark.parametrize("with_ids", [False, True])
+@pytest.mark.parametrize("heads,dim,group", [
+    (8, 128, 2), (7, 128, 1), (13, 128, 1), (5, 128, 3), (2, 128, 12), (8, 64, 2), (6, 64, 1),
+    (12, 64, 1), (4, 64, 9), (7, 64, 1), (4, 256, 2), (3, 256, 1)])
+def test_even_shares_of_all_head_counts(dk, heads, dim, group, with_ids):
+    """Heads walked together in teams, part teams, teams with nobody, scale rows
+    that are no whole 16-byte pieces; holes, windows, a row of nothing."""
+    rng = np.random.default_rng(heads * dim + group)
+    page, width = 16, 3000  # as if rows could be long: shares
+    cache, host = fill(dk, rng, 48, page, heads, dim)
+    rows = 4
+    table = table_of(rng, rows, width, 48)
+    table[0, 3], table[2, :2] = -1, [48, 2 ** 30]
+    lens, starts = np.array([700, 0, 300, 33]), np.array([5, 0, 130, 32])
+    ids = None
+    if with_ids:
+        ids = rng.integers(0, 720, (rows, 90000))
+        ids[:, ::3] = -1
+        ids[3] = -1
+        ids[:, 200:] = -1
+    q, values = query(rng, rows, heads * group, dim, "f16")
+    assert dk.kv4_attention_workspace_size(cache, rows, heads * group, width,
+                                           num_ids=90000 if with_ids else None) > 0
+    out, lse = check(dk, cache, host, q, values, "f16", table, lens, starts=starts, ids=ids)
+    w = torch.zeros(rows, 720, device=DEV)
+    out2, lse2 = dk.kv4_attention(cache, q, i32(table), i32(lens), starts=i32(starts),
+                                  ids=i32(ids), weights=w)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    _, _, want, _, _, tol = ref.attention(host, values, table, lens, ids=ids, starts=starts,
+                                          positions=720)
+    assert np.all(np.abs(w.double().cpu().numpy() - want) <= tol + 2.0 ** -23 * want)
+
+
 def test_starts_negative_lengths_and_lengths_beyond_the_table(dk):
     rng = np.random.default_rng(7)
     cache, host = fill(dk, rng, 40, 16, 2, 128)

@@ -399,12 +399,12 @@ dcp_status dcp_kv4_evict(const dcp_kv4_cache* cache, const dcp_kv4_evict_args* a
   p.recent = a->recent;
   p.row_codes = cache->heads * cache->dim / 2;
   p.row_scales = cache->heads * cache->dim / kBlock;
-  // CTAs per sequence: up to a portable cluster, while they fit on the GPU at
-  // once and have 2048 weights each
+  // CTAs per sequence: a round of weights each, up to a portable cluster.  More
+  // CTAs with fewer weights gain nothing, since each pass then pays the cluster's
+  // barrier and remote loads (32 sequences of up to 16384 weights: four CTAs each
+  // 20.4 us, one 19.8).
   int ctas = 1;
-  while (ctas < kSelMostCtas && (int64_t)ctas * 2048 < limit &&
-         (int64_t)a->num_seqs * ctas * 2 <= kPlanSms)
-    ctas *= 2;
+  while (ctas < kSelMostCtas && (int64_t)ctas * kSelRound < limit) ctas *= 2;
   cudaError_t e = launch(evict_select_kernel, dim3((unsigned)(a->num_seqs * ctas)), kSelThreads, 0,
                          ctas, (cudaStream_t)stream, p);
   if (e != cudaSuccess) return DCP_ERR_CUDA;

@@ -168,8 +168,8 @@ struct Lookup {
     return ok;
   }
   // On to tile k + 1, after the copies of tile k and in their group.  The id
-  // read here, of tile k + 2, came with the copies of tile k - 3: at least two
-  // groups are complete by then beyond those that may still be under way.
+  // read here, of tile k + 2, came with the copies of tile k - 3, whose group is
+  // complete: a ring has at most three stages.
   __device__ void advance(int k) {
     page0 = page1;
     if constexpr (kIds) {
@@ -557,7 +557,8 @@ __device__ __forceinline__ void write_out(const AttentionParams& p, int64_t at, 
 // rather than lse, whose rounding would be an error of the exponent; the
 // exponent is the attention's own, bit for bit.  8 lanes a token, 4 heads to a
 // lane's load where the rows allow it, 4 tokens of a lane in flight; a CTA per
-// 128 tokens of a row.
+// 128 tokens of a row.  8 rows of up to 16384 tokens x 64 heads: 9 us after the
+// attention, whose score writes are another 25 MB.
 constexpr int kWeightTokens = 128;
 
 template <bool kIds>

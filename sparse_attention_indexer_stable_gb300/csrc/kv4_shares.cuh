@@ -8,6 +8,13 @@
 // in memory, and DRAM serves 128 bytes at a time.  Walked one after the other,
 // 131072 tokens of 8 heads with 64-byte rows read 2.2 times their bytes.
 //
+// Measured (8 heads x 128, 8 query heads each): 256 rows of 64 to 8192 tokens
+// 233 us, 5.3 TB/s, 78% of the measured copy rate; without its copies the
+// kernel takes 189 us, without the scales' multiplications 213.  16 rows of 1
+// to 16384 tokens 46 us, two of 131072 70 us: there 12 us go by before the
+// first tile and after the last, 9 us while one of an SM's two CTAs is done and
+// the other is not, 5 to 10 in the join.
+//
 // Measured and not taken: one producer warp that copies a token's rows of all
 // heads in bulk (cp.async.bulk, 4 a token): about 60 cycles a copy, 983 us
 // against 271 us for 256 rows of up to 8192 tokens.

@@ -143,7 +143,8 @@ dcp_status dcp_kv4_attention_workspace_size(const dcp_kv4_cache* cache,
  * Errors: DCP_ERR_INVALID for a bad cache or dtype, negative sizes, q_heads
  * not a multiple of heads, a NULL required pointer with rows > 0, weights with
  * owner, or a workspace smaller than reported; DCP_ERR_UNSUPPORTED for a dim
- * or page size outside the limits, or more than 2^31 - 1 positions;
+ * or page size outside the limits, more than 2^31 - 1 positions, or weights of
+ * more than 4096 query heads;
  * DCP_ERR_CUDA if a launch fails.  rows == 0 is a no-op.
  */
 dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention_args* args,

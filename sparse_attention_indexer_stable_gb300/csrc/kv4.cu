@@ -181,6 +181,10 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
     plan->part_ml = take(pieces * sizeof(float2));
   }
   if (a->weights) {
+    // the grid and the shared memory of the kernel that adds the weights up
+    if (a->q_heads > kMostWeightHeads ||
+        a->rows * (((int64_t)plan->width + kWeightTokens - 1) / kWeightTokens) > INT_MAX)
+      return DCP_ERR_UNSUPPORTED;
     plan->scores = take(heads * plan->width * sizeof(float));
     plan->row_mult = take(heads * sizeof(float));
     plan->row_ml = take(heads * sizeof(float2));

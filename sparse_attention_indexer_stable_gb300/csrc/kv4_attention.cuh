@@ -560,6 +560,7 @@ __device__ __forceinline__ void write_out(const AttentionParams& p, int64_t at, 
 // 128 tokens of a row.  8 rows of up to 16384 tokens x 64 heads: 9 us after the
 // attention, whose score writes are another 25 MB.
 constexpr int kWeightTokens = 128;
+constexpr int kMostWeightHeads = 4096;  // 48 KB of shared memory
 
 template <bool kIds>
 __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ AttentionParams p) {

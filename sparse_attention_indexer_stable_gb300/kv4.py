@@ -181,7 +181,7 @@ def kv4_attention(cache, q, table, lens, ids=None, owner=None, starts=None, row_
     ids: int32 (T, K), as merge and fused_topk return them: the row attends
     only to these positions (those that it sees); -1 is padding.  row_starts:
     int32 (T,), subtracted from the ids, as it was added by the top-K.
-    scale: default dim ** -0.5.  softcap: scores become
+    scale: default (None or 0) dim ** -0.5.  softcap: scores become
     softcap * tanh(score / softcap); 0: none.
     weights: float32 (T, positions), unit column stride: each position's
     probability, summed over the query heads, is added (not with owner).

@@ -90,6 +90,7 @@ def test_read_wants_aligned_outputs():
     (dict(weights=FAKE), dk.DCP_ERR_INVALID),           # no workspace
     (dict(weights=FAKE, workspace=FAKE, workspace_bytes=64), dk.DCP_ERR_INVALID),
     (dict(table_width=1 << 28), dk.DCP_ERR_UNSUPPORTED),
+    (dict(weights=FAKE, q_heads=4098), dk.DCP_ERR_UNSUPPORTED),
     (dict(rows=0, q=0, lens=0, out=0, lse=0), dk.DCP_OK),
 ])
 def test_attention_argument_errors(change, want):

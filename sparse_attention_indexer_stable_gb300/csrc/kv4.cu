@@ -68,15 +68,19 @@ static cudaError_t allow_smem(Kernel* kernel, int bytes) {
 
 template <int D, int NT>
 static cudaError_t allow_attention() {
-  constexpr int kSlice = kSliceWarps * RingShape<D, NT>::kBytes;
+  constexpr int kSlice = SliceShape<D, NT, false>::kSmem;
   constexpr int kShare = ShareShape<D, NT>::kSmem;
   cudaError_t e;
-  if ((e = allow_smem(attention_slices_kernel<D, NT, false>, kSlice)) != cudaSuccess ||
-      (e = allow_smem(attention_slices_kernel<D, NT, true>, kSlice)) != cudaSuccess ||
+  if ((e = allow_smem(attention_slices_kernel<D, NT, false, false>, kSlice)) != cudaSuccess ||
+      (e = allow_smem(attention_slices_kernel<D, NT, true, false>, kSlice)) != cudaSuccess ||
       (e = allow_smem(attention_shares_kernel<D, NT, false, false>, kShare)) != cudaSuccess ||
       (e = allow_smem(attention_shares_kernel<D, NT, true, false>, kShare)) != cudaSuccess)
     return e;
-  if constexpr (D < 256) e = allow_smem(attention_shares_kernel<D, NT, true, true>, kShare);
+  if constexpr (D < 256) {
+    e = allow_smem(attention_shares_kernel<D, NT, true, true>, kShare);
+    if (e == cudaSuccess)
+      e = allow_smem(attention_slices_kernel<D, NT, true, true>, SliceShape<D, NT, true>::kSmem);
+  }
   if constexpr (D == 64)
     if (e == cudaSuccess) e = allow_smem(attention_shares_kernel<D, NT, false, true>, kShare);
   return e;
@@ -105,7 +109,8 @@ static cudaError_t prepare_device() {
 // workspace lie.
 struct Plan {
   int heads_per_cta, head_tiles, limit, width;
-  int slices;  // CTAs of a row and head, when > 0
+  int slices;  // CTAs of a row and head, or a row and team, when > 0
+  int team;    // heads of a slice
   int shares;  // even shares, when > 0
   int together;  // key/value heads that a share walks at the same time
   int cuts;    // units, where a CTA joins one head of a unit (0: a warp does)
@@ -142,10 +147,19 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   const int64_t tiles = ((int64_t)plan->width + kTile - 1) / kTile;
   const int64_t warps = c->dim * plan->heads_per_cta >= 2048 ? 8 : 16;  // of an SM
   auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  // Slices of ids in teams (kv4_team.cuh) where there are whole teams and an SM
+  // gets 20 tiles of 128 elements or more, so that lines bound it and not
+  // latency (2048 ids, 8 heads x 128, without and with teams: 4 rows 10.1 us
+  // and 11.3, 8 rows 13.1 and 12.3, 16 rows 24.3 and 17.7, 64 rows 51 and 47;
+  // 8 heads x 64, 8 rows: 9.7 and 11.1, 16 rows 13.6 and 12.0).
+  const int members = c->dim < 256 ? 256 / c->dim : 1;
+  const bool enough = units * tiles * c->dim >= (int64_t)20 * 128 * kPlanSms;
+  plan->team = a->ids && enough && c->heads % members == 0 ? members : 1;
   int64_t least = INT64_MAX;
   for (int s = 1; s <= 8; s *= 2) {
-    const int64_t steps = ceil_div(units * s, kPlanSms * warps / kSliceWarps) *
-                          (ceil_div(ceil_div(tiles, s), kSliceWarps) + kPieceCost);
+    const int64_t steps =
+        ceil_div(units / plan->team * s, kPlanSms * warps / kSliceWarps) *
+        (ceil_div(ceil_div(tiles, s), kSliceWarps / plan->team) + kPieceCost);
     if (steps < least) least = steps, plan->slices = s;
   }
   // the largest power of two that leaves at most a fifth of the warps idle
@@ -163,7 +177,9 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   // for each warp of a CTA, a CTA joins one head, otherwise a warp does.
   const int64_t cuts = a->rows * ceil_div(c->heads, plan->together) * plan->head_tiles;
   plan->cuts = cuts * 16 <= plan->shares ? (int)cuts : 0;
-  if (units * 8 > INT_MAX || units * (tiles + kPieceTiles + 1) / kPlanSms > INT_MAX || (int64_t)a->rows * a->q_heads > INT_MAX) return DCP_ERR_UNSUPPORTED;
+  if (units * 8 > INT_MAX || units * (tiles + kPieceTiles + 1) / kPlanSms > INT_MAX ||
+      (int64_t)a->rows * a->q_heads > INT_MAX)
+    return DCP_ERR_UNSUPPORTED;
   const size_t heads = (size_t)a->rows * a->q_heads;
   size_t at = 0;
   auto take = [&at](size_t bytes) {
@@ -197,11 +213,16 @@ template <int D, int NT>
 static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
                                     cudaStream_t stream) {
   if (plan.slices) {
-    const unsigned grid = (unsigned)p.rows * p.head_tiles * p.c.heads * plan.slices;
-    return launch(p.ids ? attention_slices_kernel<D, NT, true>
-                        : attention_slices_kernel<D, NT, false>,
-                  dim3(grid), kSliceThreads, kSliceWarps * RingShape<D, NT>::kBytes, plan.slices,
-                  stream, p);
+    const unsigned grid =
+        (unsigned)p.rows * p.head_tiles * (p.c.heads / plan.team) * plan.slices;
+    if constexpr (D < 256)
+      if (plan.team > 1)
+        return launch(attention_slices_kernel<D, NT, true, true>, dim3(grid), kSliceThreads,
+                      SliceShape<D, NT, true>::kSmem, plan.slices, stream, p);
+    return launch(p.ids ? attention_slices_kernel<D, NT, true, false>
+                        : attention_slices_kernel<D, NT, false, false>,
+                  dim3(grid), kSliceThreads, SliceShape<D, NT, false>::kSmem, plan.slices, stream,
+                  p);
   }
   using Shape = ShareShape<D, NT>;
   auto* kernel = p.ids ? attention_shares_kernel<D, NT, true, false>
@@ -243,8 +264,8 @@ static cudaError_t launch_all(const AttentionParams& p, int dim, const Plan& pla
   if (e != cudaSuccess || !p.weights || p.width == 0) return e;
   const int64_t tiles = ((int64_t)p.width + kWeightTokens - 1) / kWeightTokens;
   return launch(p.ids ? weights_kernel<true> : weights_kernel<false>,
-                dim3((unsigned)(p.rows * tiles)), 256, (size_t)((p.q_heads + 3) & ~3) * 3 * sizeof(float), 1,
-                stream, p);
+                dim3((unsigned)(p.rows * tiles)), 256,
+                (size_t)((p.q_heads + 3) & ~3) * 3 * sizeof(float), 1, stream, p);
 }
 
 }  // namespace kv4

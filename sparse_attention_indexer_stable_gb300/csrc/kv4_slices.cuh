@@ -3,11 +3,12 @@
 // joined through distributed shared memory.  One launch, no workspace.  Bound
 // by latency: a row of 2048 tokens is one tile per warp and slice, 7 us with 8
 // heads x 128 (with slices joined by a second kernel through a workspace 7 us
-// too, but 3 us more on the host); 16 rows x 2048 ids 24 us, of which 16 are
-// four tiles a warp, by the lines that L1 takes in (see kv4_team.cuh).
+// too, but 3 us more on the host).  16 rows x 2048 ids take 17.7 us in teams of
+// two heads (kv4_team.cuh) and 24.3 with a ring per warp: then L1 takes in lines
+// for 16 us.
 #pragma once
 
-#include "kv4_ring.cuh"
+#include "kv4_team.cuh"
 
 namespace dcp {
 namespace kv4 {
@@ -15,20 +16,28 @@ namespace kv4 {
 constexpr int kSliceWarps = 8;
 constexpr int kSliceThreads = 32 * kSliceWarps;
 
-// The join, in the ring's place: each warp's outputs (padded rows), references
+// A CTA's 8 warps work on one head, or (kTeam) in teams on neighbouring heads.
+//
+// The join, in the rings' place: each warp's outputs (padded rows), references
 // and sums, and behind them the CTA's own for the cluster (16 bytes per output
 // pair).
-template <int D, int NT>
-struct SliceJoin {
+template <int D, int NT, bool kTeam>
+struct SliceShape {
+  static constexpr int kMembers = kTeam ? TeamStage<D>::kTeam : 1;  // heads
+  static constexpr int kRings = kTeam ? kSliceWarps / kMembers * TeamShape<D, NT>::kBytes
+                                      : kSliceWarps * RingShape<D, NT>::kBytes;
   static constexpr int kStride = D + 4;
   static constexpr int kWarpBytes = (kSliceWarps * 8 * NT * (kStride + 2) * 4 + 15) & ~15;
-  static_assert(kWarpBytes + 8 * NT * D / 2 * 16 <= kSliceWarps * RingShape<D, NT>::kBytes, "fits the ring");
+  static constexpr int kJoin = kWarpBytes + kMembers * 8 * NT * D / 2 * 16;
+  static constexpr int kSmem = kRings > kJoin ? kRings : kJoin;
+  static constexpr int kPerSm = RingShape<D, NT>::kWarpsPerSm / kSliceWarps;  // CTAs
+  static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // Leaves a warp's sums in shared memory (all warps of the CTA: barriers).
 template <int D, int NT>
 __device__ __forceinline__ void leave_sums(const Heads<D, NT>& hd, uint8_t* smem) {
-  using Join = SliceJoin<D, NT>;
+  using Join = SliceShape<D, NT, false>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
   __syncthreads();  // every warp has read its ring
@@ -53,20 +62,21 @@ __device__ __forceinline__ void leave_sums(const Heads<D, NT>& hd, uint8_t* smem
   __syncthreads();
 }
 
-// What leave_sums left, added over the warps: reference, sum and two outputs
-// of `head` at element d.
-template <int D, int NT>
-__device__ __forceinline__ Joined join_warps(const uint8_t* smem, int head, int d) {
-  using Join = SliceJoin<D, NT>;
+// What leave_sums left, added over the warps first, first + step, ...:
+// reference, sum and two outputs of `head` at element d.
+template <int D, int NT, int kStep>
+__device__ __forceinline__ Joined join_warps(const uint8_t* smem, int first, int head, int d) {
+  using Join = SliceShape<D, NT, false>;
   const float* join_o = reinterpret_cast<const float*>(smem);
   const float* join_m = join_o + kSliceWarps * 8 * NT * Join::kStride;
   const float* join_l = join_m + kSliceWarps * 8 * NT;
   Joined j{kNoScore, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int w = 0; w < kSliceWarps; ++w) j.top = fmaxf(j.top, join_m[w * 8 * NT + head]);
+  for (int w = 0; w < kSliceWarps; w += kStep)
+    j.top = fmaxf(j.top, join_m[(first + w) * 8 * NT + head]);
 #pragma unroll
-  for (int w = 0; w < kSliceWarps; ++w) {
-    const int col = w * 8 * NT + head;
+  for (int w = 0; w < kSliceWarps; w += kStep) {
+    const int col = (first + w) * 8 * NT + head;
     const float f = exp2_approx(join_m[col] - j.top);
     const float2 v = *reinterpret_cast<const float2*>(join_o + col * Join::kStride + d);
     j.sum += f * join_l[col];
@@ -76,21 +86,26 @@ __device__ __forceinline__ Joined join_warps(const uint8_t* smem, int head, int 
   return j;
 }
 
-// blockIdx.x = ((row * head_tiles + head tile) * heads + head) * slices + slice.
-template <int D, int NT, bool kIds>
-__global__ void __launch_bounds__(kSliceThreads, RingShape<D, NT>::kWarpsPerSm / kSliceWarps)
+// blockIdx.x = ((row * head_tiles + head tile) * groups + group) * slices +
+// slice; a group is a head, or a team's heads.
+template <int D, int NT, bool kIds, bool kTeam>
+__global__ void __launch_bounds__(kSliceThreads, SliceShape<D, NT, kTeam>::kPerSm)
     attention_slices_kernel(const __grid_constant__ AttentionParams p) {
   namespace cg = cooperative_groups;
+  using Shape = SliceShape<D, NT, kTeam>;
+  constexpr int kMembers = Shape::kMembers;
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int slices = (int)cluster.num_blocks(), slice = (int)cluster.block_rank();
   const unsigned unit = blockIdx.x / (unsigned)slices;
-  const int h = (int)(unit % (unsigned)p.c.heads);
-  const unsigned rest = unit / (unsigned)p.c.heads;
+  const unsigned groups = (unsigned)p.c.heads / kMembers;  // teams: the host divides evenly
+  const int h0 = (int)(unit % groups) * kMembers;
+  const unsigned rest = unit / groups;
   const int ht = (int)(rest % (unsigned)p.head_tiles);
   const int t = (int)(rest / (unsigned)p.head_tiles);
-  const int head0 = h * p.group + ht * 8 * NT;           // first query head of this CTA
-  const int heads = min(8 * NT, p.group - ht * 8 * NT);  // and how many
+  const int heads = min(8 * NT, p.group - ht * 8 * NT);  // query heads of each
+  const int warp = threadIdx.x >> 5, member = warp % kMembers;
+  const int head0 = (h0 + member) * p.group + ht * 8 * NT;  // first query head of this warp
 
   grid_dependency_wait();
   const RowSpan r = row_span<kIds>(p, t);
@@ -98,26 +113,36 @@ __global__ void __launch_bounds__(kSliceThreads, RingShape<D, NT>::kWarpsPerSm /
   const int per = (tiles + slices - 1) / slices;
   const int tile0 = min(tiles, slice * per), tile1 = min(tiles, tile0 + per);
   Heads<D, NT> hd;
-  attend_tiles<D, NT, kIds>(p, r, t, h, head0, heads, tile0, tile1, threadIdx.x >> 5, kSliceWarps,
-                            smem, hd);
+  if constexpr (kTeam)
+    attend_team<D, NT, kIds>(p, r, t, h0, kMembers, member, true, head0, heads, tile0, tile1,
+                             warp / kMembers, kSliceWarps / kMembers, smem, hd);
+  else
+    attend_tiles<D, NT, kIds>(p, r, t, h0, head0, heads, tile0, tile1, warp, kSliceWarps, smem,
+                              hd);
   leave_sums<D, NT>(hd, smem);
 
-  const int64_t at = (int64_t)t * p.q_heads + head0;
+  // output pairs of the CTA: member, query head, element
+  const int pairs = kMembers * heads * (D / 2);
+  auto join_pair = [&](int i) {
+    const int q = i / (D / 2);
+    return join_warps<D, NT, kMembers>(smem, kMembers == 1 ? 0 : q / heads, q % heads,
+                                       2 * (i % (D / 2)));
+  };
+  auto write_pair = [&](int i, const Joined& j) {
+    const int q = i / (D / 2);
+    const int64_t at = (int64_t)t * p.q_heads + (h0 + q / heads) * p.group + ht * 8 * NT;
+    write_out<D>(p, at + q % heads, 2 * (i % (D / 2)), j);
+  };
   if (slices == 1) {
-    for (int i = threadIdx.x; i < heads * (D / 2); i += kSliceThreads) {
-      const int head = i / (D / 2), d = 2 * (i % (D / 2));
-      write_out<D>(p, at + head, d, join_warps<D, NT>(smem, head, d));
-    }
+    for (int i = threadIdx.x; i < pairs; i += kSliceThreads) write_pair(i, join_pair(i));
     return;
   }
   // The CTA's own join goes behind the warps' (each thread its own values),
   // then every CTA adds its part of the outputs over the cluster.
-  Joined* mine = reinterpret_cast<Joined*>(smem + SliceJoin<D, NT>::kWarpBytes);
-  for (int i = threadIdx.x; i < heads * (D / 2); i += kSliceThreads)
-    mine[i] = join_warps<D, NT>(smem, i / (D / 2), 2 * (i % (D / 2)));
+  Joined* mine = reinterpret_cast<Joined*>(smem + Shape::kWarpBytes);
+  for (int i = threadIdx.x; i < pairs; i += kSliceThreads) mine[i] = join_pair(i);
   cluster.sync();
-  for (int i = slice * kSliceThreads + threadIdx.x; i < heads * (D / 2);
-       i += slices * kSliceThreads) {
+  for (int i = slice * kSliceThreads + threadIdx.x; i < pairs; i += slices * kSliceThreads) {
     Joined j{kNoScore, 0.0f, 0.0f, 0.0f};
     Joined other[8];
 #pragma unroll
@@ -134,7 +159,7 @@ __global__ void __launch_bounds__(kSliceThreads, RingShape<D, NT>::kWarpsPerSm /
         j.x += f * other[c].x;
         j.y += f * other[c].y;
       }
-    write_out<D>(p, at + i / (D / 2), 2 * (i % (D / 2)), j);
+    write_pair(i, j);
   }
   cluster.sync();  // no CTA leaves while others read its shared memory
 }

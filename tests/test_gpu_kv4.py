@@ -371,6 +371,41 @@ def test_selected_ids(dk, owned, dim, heads, group, num_ids):
           row_starts=row_starts, starts=np.array([0, 20, 0, 0, 0]))
 
 
+@pytest.mark.parametrize("heads,dim,group,rows,num_ids", [
+    (8, 128, 2, 75, 300), (2, 128, 7, 160, 623), (2, 128, 12, 100, 511), (2, 128, 40, 50, 330),
+    (4, 64, 3, 120, 821), (8, 64, 9, 50, 512), (8, 128, 1, 9, 2048), (4, 64, 1, 24, 2500),
+    (6, 128, 3, 40, 1000)])
+def test_selected_ids_of_many_short_rows(dk, heads, dim, group, rows, num_ids):
+    """Neighbouring heads' warps copy together: rows of one to many tiles of 32
+    ids, rows of nothing, windows, holes, padding, head tiles; whole rows to a
+    CTA and rows split over a cluster."""
+    rng = np.random.default_rng(heads * dim + group)
+    cache, host = fill(dk, rng, 100, 16, heads, dim)
+    table = table_of(rng, rows, 60, 100)
+    table[0, 3], table[2, :2] = -1, [100, 2 ** 30]
+    lens = rng.integers(1, 960, rows)
+    lens[[1, 4]] = [0, 1]
+    starts = np.where(rng.random(rows) < 0.5, lens // 3, 0)
+    ids = rng.integers(0, 960, (rows, num_ids))
+    ids[:, ::5] = -1
+    ids[3] = -1
+    ids[5, 33:] = -1
+    ids[6:8, :num_ids // 2] = -1
+    q, values = query(rng, rows, heads * group, dim, "bf16")
+    # slices: no workspace; enough of them for teams
+    assert dk.kv4_attention_workspace_size(cache, rows, heads * group, 60, num_ids=num_ids) == 0
+    width = 8 if group <= 8 else 16
+    assert rows * heads * -(-group // width) * -(-num_ids // 32) * dim >= 20 * 128 * 152
+    out, lse = check(dk, cache, host, q, values, "bf16", table, lens, starts=starts, ids=ids)
+    w = torch.zeros(rows, 960, device=DEV)
+    out2, lse2 = dk.kv4_attention(cache, q, i32(table), i32(lens), starts=i32(starts),
+                                  ids=i32(ids), weights=w)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    _, _, want, _, _, tol = ref.attention(host, values, table, lens, ids=ids, starts=starts,
+                                          positions=960)
+    assert np.all(np.abs(w.double().cpu().numpy() - want) <= tol + 2.0 ** -23 * want)
+
+
 def test_ids_and_row_starts_at_the_ends_of_int32(dk):
     rng = np.random.default_rng(15)
     cache, host = fill(dk, rng, 8, 16, 1, 64)

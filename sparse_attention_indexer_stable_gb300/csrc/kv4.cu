@@ -242,12 +242,17 @@ static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
                                1, stream, p);
   if (e != cudaSuccess) return e;
   const int heads = p.together * 8 * NT;
-  return plan.cuts ? launch(join_shares_kernel<D, NT, true>,
-                            dim3((unsigned)plan.cuts, (unsigned)heads), 32 * kJoinWarps, 0, 1,
-                            stream, p)
-                   : launch(join_shares_kernel<D, NT, false>,
-                            dim3((unsigned)plan.shares, (unsigned)(heads / kJoinWarps)),
-                            32 * kJoinWarps, 0, 1, stream, p);
+  if (!plan.cuts)
+    return launch(join_shares_kernel<D, NT, false>,
+                  dim3((unsigned)plan.shares, (unsigned)(heads / kJoinWarps)), 32 * kJoinWarps, 0,
+                  1, stream, p);
+  // By unit, as many warps to a query head as the SMs hold at the same time (32
+  // each): two rows of 131072 tokens 75, 68, 66, 64 us with 4, 8, 16, 32 warps,
+  // 16 rows of up to 16384 43, 45, 51, 62.
+  int warps = kMostJoinWarps;
+  while (warps > kLeastJoinWarps && plan.cuts * heads * warps > kPlanSms * 32) warps /= 2;
+  return launch(join_shares_kernel<D, NT, true>, dim3((unsigned)plan.cuts, (unsigned)heads),
+                32 * warps, 0, 1, stream, p);
 }
 
 static cudaError_t launch_all(const AttentionParams& p, int dim, const Plan& plan,

@@ -10,15 +10,17 @@
 //
 // Measured (8 heads x 128, 8 query heads each): 256 rows of 64 to 8192 tokens
 // 233 us, 5.3 TB/s, 78% of the measured copy rate; without its copies the
-// kernel takes 189 us, without the scales' multiplications 213.  16 rows of 1
-// to 16384 tokens 46 us, two of 131072 70 us: there 12 us go by before the
-// first tile and after the last, 9 us while one of an SM's two CTAs is done and
-// the other is not, 5 to 10 in the join.
+// kernel takes 189 us, without anything but its copies 212, without the scales'
+// multiplications 213.  16 rows of 1 to 16384 tokens 43 us, two of 131072 64 us:
+// there 12 us go by before the first tile and after the last, 9 us while one of
+// an SM's two CTAs is done and the other is not, 4 in the join.
 //
 // Measured and not taken: one producer warp that copies a token's rows of all
 // heads in bulk (cp.async.bulk, 4 a token): about 60 cycles a copy, 983 us
 // against 271 us for 256 rows of up to 8192 tokens.
 #pragma once
+
+#include <type_traits>
 
 #include "kv4_team.cuh"
 
@@ -247,16 +249,18 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
 // Joins the pieces of a unit that shares cut.  kByUnit: a CTA per unit and
 // query head (few units of many pieces), its warps dealt the pieces.  Otherwise
 // a CTA per share (for the unit whose first piece is the share's last) and 8
-// query heads, a warp each.  A lane holds D / 32 contiguous elements.
+// query heads, a warp each.  A lane holds D / 32 contiguous elements; a piece's
+// outputs are loaded together with its reference, a batch of pieces at a time.
 constexpr int kJoinWarps = 8;
+constexpr int kLeastJoinWarps = 4, kMostJoinWarps = 32;  // of a CTA, kByUnit
 
 template <int D, int NT, bool kByUnit>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(32 * (kByUnit ? kMostJoinWarps : kJoinWarps))
     join_shares_kernel(const __grid_constant__ AttentionParams p) {
   constexpr int kPer = D / 32;
-  constexpr int kWays = kByUnit ? kJoinWarps : 1;
-  __shared__ float red[kWays][D];
-  __shared__ float2 red_ml[kWays];
+  __shared__ float red[kByUnit ? kMostJoinWarps : 1][D];
+  __shared__ float2 red_ml[kByUnit ? kMostJoinWarps : 1];
+  const int ways = kByUnit ? blockDim.x / 32 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (p.c.heads + p.together - 1) / p.together;
   const int units = groups * p.head_tiles;
@@ -285,34 +289,45 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   float acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
-  for (int i0 = c + (kByUnit ? warp : 0); i0 <= last; i0 += 32 * kWays) {
-    const int mine = i0 + lane * kWays;
+  constexpr int kBatch = kByUnit && D < 256 ? 4 : 2;  // pieces
+  using Row = typename std::conditional<kPer == 2, float2, float4>::type;
+  constexpr int kRows = kPer * 4 / (int)sizeof(Row);
+  for (int i0 = c + (kByUnit ? warp : 0); i0 <= last; i0 += 32 * ways) {
+    const int count = min(32, (last - i0) / ways + 1);
+    const int mine = i0 + lane * ways;
+    Row w[kBatch][kRows];
+    auto load = [&](int k0) {  // beyond the last piece: that once more, times 0
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + min(k0 + k, count - 1) * ways;
+        const float* src = p.part_out + piece(i) * D + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kRows; ++e) w[k][e] = reinterpret_cast<const Row*>(src)[e];
+      }
+    };
+    load(0);
     const float2 ml = mine <= last ? p.part_ml[piece(mine)] : make_float2(kNoScore, 0.0f);
     float top = ml.x;
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     top = fmaxf(top, j.top);
-    const float scale = exp2_approx(j.top - top), f = exp2_approx(ml.x - top);
+    const float scale = exp2_approx(j.top - top);
+    const float f = mine <= last ? exp2_approx(ml.x - top) : 0.0f;
     j.top = top;
     j.sum = j.sum * scale + f * ml.y;  // of this lane's pieces
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] *= scale;
-    const int count = min(32, (last - i0) / kWays + 1);
-#pragma unroll 8
-    for (int k = 0; k < count; ++k) {
-      const float* src = p.part_out + piece(i0 + k * kWays) * D + lane * kPer;
-      const float fk = __shfl_sync(0xffffffffu, f, k);
-      if constexpr (kPer == 2) {
-        const float2 w = *reinterpret_cast<const float2*>(src);
-        acc[0] += fk * w.x, acc[1] += fk * w.y;
-      } else {
+    for (int k0 = 0;;) {
 #pragma unroll
-        for (int e = 0; e < kPer; e += 4) {
-          const float4 w = *reinterpret_cast<const float4*>(src + e);
-          acc[e] += fk * w.x, acc[e + 1] += fk * w.y;
-          acc[e + 2] += fk * w.z, acc[e + 3] += fk * w.w;
-        }
+      for (int k = 0; k < kBatch; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          acc[e] += fk * reinterpret_cast<const float*>(w[k])[e];
       }
+      k0 += kBatch;
+      if (k0 >= count) break;
+      load(k0);
     }
   }
 #pragma unroll
@@ -324,12 +339,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     if (lane == 0) red_ml[warp] = make_float2(j.top, j.sum);
     __syncthreads();
     j = Joined{kNoScore, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kWays; ++w) j.top = fmaxf(j.top, red_ml[w].x);
-    for (int d = 2 * threadIdx.x; d < D; d += 64 * kJoinWarps) {
+    for (int w = 0; w < ways; ++w) j.top = fmaxf(j.top, red_ml[w].x);
+    for (int d = 2 * threadIdx.x; d < D; d += 2 * blockDim.x) {
       j.sum = j.x = j.y = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWays; ++w) {
+#pragma unroll 4
+      for (int w = 0; w < ways; ++w) {
         const float f = exp2_approx(red_ml[w].x - j.top);
         j.sum += f * red_ml[w].y;
         j.x += f * red[w][d];

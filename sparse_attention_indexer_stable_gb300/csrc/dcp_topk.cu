@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 
-static cudaError_t status_word(unsigned int** out) {
+cudaError_t device_status_word(unsigned int** out) {
   return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_device_status);
 }
 
@@ -469,7 +469,7 @@ static cudaError_t device_info(DeviceInfo** out) {
     if ((e = allow_max_smem(merge_rows_kernel<ShardsSource>, (int)sizeof(RowsShared))) !=
         cudaSuccess)
       return e;
-    if ((e = status_word(&d.status)) != cudaSuccess) return e;
+    if ((e = device_status_word(&d.status)) != cudaSuccess) return e;
     d.configured.store(true, std::memory_order_release);
   }
   *out = &d;
@@ -704,7 +704,7 @@ dcp_status dcp_fused_topk(const float* logits, int T, int dcp_, int L, int ld, i
 dcp_status dcp_topk_device_status(unsigned int* status) {
   if (!status) return DCP_ERR_INVALID;
   unsigned int* word = nullptr;
-  if (dcp::status_word(&word) != cudaSuccess) return DCP_ERR_CUDA;
+  if (dcp::device_status_word(&word) != cudaSuccess) return DCP_ERR_CUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return DCP_ERR_CUDA;
   unsigned int v = 0u;
   if (cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return DCP_ERR_CUDA;
@@ -717,7 +717,7 @@ dcp_status dcp_topk_device_status(unsigned int* status) {
 
 dcp_status dcp_topk_selftest_wait_timeout(unsigned int wait_cycles, dcp_stream_t stream) {
   unsigned int* word = nullptr;
-  if (dcp::status_word(&word) != cudaSuccess) return DCP_ERR_CUDA;
+  if (dcp::device_status_word(&word) != cudaSuccess) return DCP_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1u);
   cfg.blockDim = dim3(32u);

@@ -59,6 +59,7 @@ static dcp_status status_of(cudaError_t e) { return e == cudaSuccess ? DCP_OK : 
 
 // -------------------------------------------------------------- attention
 static std::atomic<bool> g_ready[64];
+static unsigned int* g_status[64];  // each device's status word, before g_ready
 static std::mutex g_dev_mutex;
 
 template <typename Kernel>
@@ -73,27 +74,36 @@ static cudaError_t allow_attention() {
   cudaError_t e;
   if ((e = allow_smem(attention_slices_kernel<D, NT, false, false>, kSlice)) != cudaSuccess ||
       (e = allow_smem(attention_slices_kernel<D, NT, true, false>, kSlice)) != cudaSuccess ||
-      (e = allow_smem(attention_shares_kernel<D, NT, false, false>, kShare)) != cudaSuccess ||
-      (e = allow_smem(attention_shares_kernel<D, NT, true, false>, kShare)) != cudaSuccess)
+      (e = allow_smem(attention_shares_kernel<D, NT, false, kByRing>, kShare)) != cudaSuccess ||
+      (e = allow_smem(attention_shares_kernel<D, NT, true, kByRing>, kShare)) != cudaSuccess ||
+      (e = allow_smem(attention_shares_kernel<D, NT, false, 8>, PageStage<D, 8>::kSmem)) !=
+          cudaSuccess)
     return e;
+  if constexpr (D > 64) {
+    e = allow_smem(attention_shares_kernel<D, NT, false, 4>, PageStage<D, 4>::kSmem);
+    if (e != cudaSuccess) return e;
+  }
   if constexpr (D < 256) {
-    e = allow_smem(attention_shares_kernel<D, NT, true, true>, kShare);
+    e = allow_smem(attention_shares_kernel<D, NT, true, kByTeam>, kShare);
     if (e == cudaSuccess)
       e = allow_smem(attention_slices_kernel<D, NT, true, true>, SliceShape<D, NT, true>::kSmem);
   }
   if constexpr (D == 64)
-    if (e == cudaSuccess) e = allow_smem(attention_shares_kernel<D, NT, false, true>, kShare);
+    if (e == cudaSuccess) e = allow_smem(attention_shares_kernel<D, NT, false, kByTeam>, kShare);
   return e;
 }
 
 // Per-device kernel attributes, set once (the first call on a device must
 // therefore not be inside a stream capture).
-static cudaError_t prepare_device() {
+static cudaError_t prepare_device(unsigned int** status) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (g_ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  if (g_ready[dev].load(std::memory_order_acquire)) {
+    *status = g_status[dev];
+    return cudaSuccess;
+  }
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   if ((e = allow_attention<64, 1>()) != cudaSuccess ||
       (e = allow_attention<64, 2>()) != cudaSuccess ||
@@ -101,6 +111,8 @@ static cudaError_t prepare_device() {
       (e = allow_attention<128, 2>()) != cudaSuccess ||
       (e = allow_attention<256, 1>()) != cudaSuccess)
     return e;
+  if ((e = device_status_word(&g_status[dev])) != cudaSuccess) return e;
+  *status = g_status[dev];
   g_ready[dev].store(true, std::memory_order_release);
   return cudaSuccess;
 }
@@ -177,7 +189,7 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   // for each warp of a CTA, a CTA joins one head, otherwise a warp does.
   const int64_t cuts = a->rows * ceil_div(c->heads, plan->together) * plan->head_tiles;
   plan->cuts = cuts * 16 <= plan->shares ? (int)cuts : 0;
-  if (units * 8 > INT_MAX || units * (tiles + kPieceTiles + 1) / kPlanSms > INT_MAX ||
+  if (units * 8 > INT_MAX || units * (tiles + kPieceTiles + 2) / kPlanSms > INT_MAX ||
       (int64_t)a->rows * a->q_heads > INT_MAX)
     return DCP_ERR_UNSUPPORTED;
   const size_t heads = (size_t)a->rows * a->q_heads;
@@ -225,21 +237,35 @@ static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
                   p);
   }
   using Shape = ShareShape<D, NT>;
-  auto* kernel = p.ids ? attention_shares_kernel<D, NT, true, false>
-                       : attention_shares_kernel<D, NT, false, false>;
+  auto* kernel = p.ids ? attention_shares_kernel<D, NT, true, kByRing>
+                       : attention_shares_kernel<D, NT, false, kByRing>;
+  size_t smem = Shape::kSmem;
   // Teams of heads whose codes fill a line, where the heads walked together are
   // whole teams, for tokens by ids (1024 rows x 2048 ids, 8 heads x 128: 518 us
   // against 539) and at dim 64 (33 rows of 12 heads: 23 us against 25).  With
   // ranges at dim 128 their barriers cost more than the lines saved: 248 us
-  // against 233 for 256 rows of up to 8192 tokens.
+  // against 232 for 256 rows of up to 8192 tokens.
   if constexpr (D < 256)
     if (p.ids && p.together % Shape::kTeam == 0)
-      kernel = attention_shares_kernel<D, NT, true, true>;
+      kernel = attention_shares_kernel<D, NT, true, kByTeam>;
   if constexpr (D == 64)
     if (!p.ids && p.together % Shape::kTeam == 0)
-      kernel = attention_shares_kernel<D, NT, false, true>;
-  const cudaError_t e = launch(kernel, dim3((unsigned)plan.shares), Shape::kThreads, Shape::kSmem,
-                               1, stream, p);
+      kernel = attention_shares_kernel<D, NT, false, kByTeam>;
+  // Ranges of caches whose runs of 8 tokens are 2 KB of codes or more, 8 heads
+  // or 4 (256 rows as above, with a ring or teams and by runs: 8 heads x 64 159
+  // us and 141, x 128 232 and 210, x 256 427 and 396; 4 heads x 128 128 and 121,
+  // x 256 230 and 220; but 4 heads x 64 84 and 85, 2 heads x 256 139 and 147).
+  if (!p.ids && p.c.page_shift >= 3 && p.c.heads == 8) {
+    kernel = attention_shares_kernel<D, NT, false, 8>;
+    smem = PageStage<D, 8>::kSmem;
+  }
+  if constexpr (D > 64)
+    if (!p.ids && p.c.page_shift >= 3 && p.c.heads == 4) {
+      kernel = attention_shares_kernel<D, NT, false, 4>;
+      smem = PageStage<D, 4>::kSmem;
+    }
+  const cudaError_t e = launch(kernel, dim3((unsigned)plan.shares), Shape::kThreads, smem, 1,
+                               stream, p);
   if (e != cudaSuccess) return e;
   const int heads = p.together * 8 * NT;
   if (!plan.cuts)
@@ -391,7 +417,7 @@ dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention
   p.score_pairs = a->q_heads % 2 == 0 && p.group % 2 == 0;
   p.scale = (a->scale != 0.0f ? a->scale : 1.0f / sqrtf((float)cache->dim)) * cache->k_unit;
   p.softcap = a->softcap;
-  if (prepare_device() != cudaSuccess) return DCP_ERR_CUDA;
+  if (prepare_device(&p.status) != cudaSuccess) return DCP_ERR_CUDA;
   return status_of(launch_all(p, cache->dim, plan, (cudaStream_t)stream));
 }
 

@@ -70,6 +70,7 @@ struct AttentionParams {
   int limit;          // positions end here at the latest
   int num_ids;
   int width;          // tokens per row of `scores`
+  unsigned int* status;  // the device's status word
   bool q_vec;
   bool score_pairs;   // two heads' scores can be stored at once
   float scale;        // of q.k, the K unit folded in
@@ -80,6 +81,7 @@ struct AttentionParams {
 // those inside count.
 struct RowSpan {
   int seq, start, end, n;
+  int skip;  // of the n, the first that the row does not see
 };
 
 template <bool kIds>
@@ -90,6 +92,7 @@ __device__ __forceinline__ RowSpan row_span(const AttentionParams& p, int t) {
   r.end = min(__ldg(p.lens + t), p.limit);
   if ((unsigned)r.seq >= (unsigned)p.num_seqs) r.seq = 0, r.end = 0;
   r.n = r.end > r.start ? (kIds ? p.num_ids : r.end - r.start) : 0;
+  r.skip = 0;
   return r;
 }
 
@@ -334,15 +337,24 @@ struct Heads {
   }
 };
 
+// All ones if the token of the V row (u, i) is there, else 0.
+template <typename At>
+__device__ __forceinline__ uint32_t present(const At& at, int u, int i, uint32_t mask) {
+  return 0u - ((mask >> at.v_token(u, i)) & 1u);
+}
+
 // One tile.  `at` says where this thread's operands lie:
-//   k(u, i), k_second(u, i): the codes of row i of sub-tile u (16 tokens), row
-//     0 token 16u + kRow(g), row 1 the token 8 later; 16 bytes (8 at dim 64),
-//     and at dim 256 16 more
+//   k(u, i), k_second(u, i): the codes of row i of sub-tile u (16 tokens), token
+//     kSubStep u + kHalfStep i + token(g); 16 bytes (8 at dim 64), and at dim 256
+//     16 more
 //   k_scale(u, i): its scales, two bytes (one at dim 64), the second pair of
 //     dim 256 8 bytes on
 //   v(u, i): dim/16 bytes of the V rows of the tokens that rows 2tq, 2tq + 1,
 //     2tq + 8, 2tq + 9 of the accumulator stand for
 //   v_scale(u, i): their scales (two bytes at dim 256, else one)
+//   k_read(), v_wait(): called when K has been read and before V is
+//   kRaw: absent tokens' rows hold anything, so their V scales are taken as 0;
+//     else they are zeros
 // j0: the tile's first token among the row's.
 template <int D, int NT, typename At>
 __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowSpan& r, int t,
@@ -351,7 +363,7 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
   constexpr int kMTiles = D / 16;
   constexpr int kSub = kTile / 16;
   const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  // S^T: rows are tokens 16u + At::token(g) and + 8, columns the heads 2tq and 2tq + 1
+  // S^T: rows are tokens (see k above), columns the heads 2tq and 2tq + 1
   float s[NT][kSub][4];
 #pragma unroll
   for (int u = 0; u < kSub; ++u) {
@@ -400,6 +412,8 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
     }
   }
 
+  at.k_read();
+
   if (p.softcap > 0.0f) {
     const float cap = p.softcap * kLog2e;
 #pragma unroll
@@ -414,7 +428,7 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
     for (int u = 0; u < kSub; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (!((mask >> (16 * u + At::token(g) + 8 * (e >> 1))) & 1u))
+        if (!((mask >> (At::kSubStep * u + At::token(g) + At::kHalfStep * (e >> 1))) & 1u))
 #pragma unroll
           for (int n = 0; n < NT; ++n) s[n][u][e] = -INFINITY;
   }
@@ -423,9 +437,10 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
     for (int u = 0; u < kSub; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t tok = j0 + 16 * u + At::token(g) + 8 * i;
+        int64_t tok = j0 + At::kSubStep * u + At::token(g) + At::kHalfStep * i;
+        if constexpr (At::kRaw) tok -= r.skip;
         float* dst = p.scores + ((int64_t)t * p.width + tok) * p.q_heads + head0 + 2 * tq;
-        if (tok < r.n)
+        if (At::kRaw ? tok >= 0 && tok < r.n - r.skip : tok < r.n)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const int head = 8 * n + 2 * tq;
@@ -484,6 +499,7 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
       pf[n][u][1] = transpose8x8(pack_pair(s[n][u][2], s[n][u][3], DCP_F16));
     }
 
+  at.v_wait();
   // O^T: rows are elements g * D/8 + 2i and + 1 (tile i), columns heads
 #pragma unroll
   for (int u = 0; u < kSub; ++u) {
@@ -498,12 +514,19 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
       const uint8_t* x = at.v_scale(u, 2 * i);
       const uint8_t* y = at.v_scale(u, 2 * i + 1);
       if constexpr (D == 256) {
-        const uint32_t a = *reinterpret_cast<const uint16_t*>(x);
-        const uint32_t b = *reinterpret_cast<const uint16_t*>(y);
+        uint32_t a = *reinterpret_cast<const uint16_t*>(x);
+        uint32_t b = *reinterpret_cast<const uint16_t*>(y);
+        if constexpr (At::kRaw)
+          if (mask != 0xffffffffu)
+            a &= present(at, u, 2 * i, mask), b &= present(at, u, 2 * i + 1, mask);
         vs[i][0] = scales_to_half(__byte_perm(a, b, 0x0040));
         vs[i][1] = scales_to_half(__byte_perm(a, b, 0x0051));
       } else {
-        vs[i][0] = scales_to_half((uint32_t)x[0] + (uint32_t)y[0] * 256u);
+        uint32_t a = x[0], b = y[0];
+        if constexpr (At::kRaw)
+          if (mask != 0xffffffffu)
+            a &= present(at, u, 2 * i, mask), b &= present(at, u, 2 * i + 1, mask);
+        vs[i][0] = scales_to_half(a + b * 256u);
       }
     }
 #pragma unroll

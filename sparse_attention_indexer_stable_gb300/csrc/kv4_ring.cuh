@@ -45,6 +45,10 @@ template <int D>
 struct RingAt {
   using S = Stage<D>;
   const uint8_t *k0, *k1, *v0, *ks0, *vs0;
+  static constexpr int kSubStep = 16, kHalfStep = 8;  // tokens
+  static constexpr bool kRaw = false;
+  __device__ void k_read() const {}
+  __device__ void v_wait() const {}
 
   // The token (of 8) of the accumulator's row i: bits 0 and 1 swapped, so that
   // the rows that a warp reads at once lie in different banks.

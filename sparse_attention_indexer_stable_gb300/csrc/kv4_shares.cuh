@@ -9,11 +9,9 @@
 // 131072 tokens of 8 heads with 64-byte rows read 2.2 times their bytes.
 //
 // Measured (8 heads x 128, 8 query heads each): 256 rows of 64 to 8192 tokens
-// 233 us, 5.3 TB/s, 78% of the measured copy rate; without its copies the
-// kernel takes 189 us, without anything but its copies 212, without the scales'
-// multiplications 213.  16 rows of 1 to 16384 tokens 43 us, two of 131072 64 us:
-// there 12 us go by before the first tile and after the last, 9 us while one of
-// an SM's two CTAs is done and the other is not, 4 in the join.
+// 210 us, 5.8 TB/s, 86% of the measured copy rate (see kv4_pages.cuh).  16 rows
+// of 1 to 16384 tokens 38 us, two of 131072 58 us: there 10 us go by before the
+// first tile and after the last, 4 in the join.
 //
 // Measured and not taken: one producer warp that copies a token's rows of all
 // heads in bulk (cp.async.bulk, 4 a token): about 60 cycles a copy, 983 us
@@ -22,7 +20,7 @@
 
 #include <type_traits>
 
-#include "kv4_team.cuh"
+#include "kv4_pages.cuh"
 
 namespace dcp {
 namespace kv4 {
@@ -41,7 +39,9 @@ struct ShareShape {
   static constexpr int kSmem = D < 256 && kTeams > kRings ? kTeams : kRings;
   // a warp's sums on their way to another: outputs, references, sums
   static constexpr int kStateWords = NT * (D / 16 * 4 + 4);
-  static_assert(kWarps / 2 * kStateWords * 32 * 4 <= kSmem, "in the ring's place");
+  static constexpr int kExchange = kWarps / 2 * kStateWords * 32 * 4;
+  static_assert(kExchange <= kSmem && kExchange <= PageStage<D, 4>::kRings,
+                "in the ring's place");
 };
 constexpr int kMostTogether = 8;  // key/value heads
 
@@ -62,13 +62,28 @@ struct Share {
 };
 constexpr int kPieceTiles = 2;
 
+// How a share walks its tiles: with a ring per warp, in teams, or in groups of
+// kWalk >= kByPages warps, for caches of as many heads (kv4_pages.cuh).
+constexpr int kByRing = 0, kByTeam = 1, kByPages = 2;
+
+// A row as shares walk it: in groups from a multiple of 8 on.
+template <bool kIds, int kWalk>
+__device__ __forceinline__ RowSpan share_span(const AttentionParams& p, int t) {
+  RowSpan r = row_span<kIds>(p, t);
+  if constexpr (kWalk >= kByPages) {
+    if (r.n > 0) r.skip = r.start & 7;
+    r.start -= r.skip, r.n += r.skip;
+  }
+  return r;
+}
+
 __device__ __forceinline__ int places_of(const RowSpan& r) {
   return kPieceTiles + max(1, (int)(((int64_t)r.n + kTile - 1) / kTile));
 }
 
 // This CTA's share, by prefix sums of the rows' places, each thread a run of
 // rows.  Barriers: the whole CTA takes part.
-template <bool kIds, int kWarps>
+template <bool kIds, int kWalk, int kWarps>
 __device__ __forceinline__ Share find_share(const AttentionParams& p, int units, int of) {
   __shared__ long long warp_sum[kWarps];
   __shared__ Share share;
@@ -77,7 +92,7 @@ __device__ __forceinline__ Share find_share(const AttentionParams& p, int units,
   const int run = (p.rows + kThreads - 1) / kThreads;
   const int row0 = min(p.rows, (int)threadIdx.x * run), row1 = min(p.rows, row0 + run);
   long long own = 0;
-  for (int t = row0; t < row1; ++t) own += places_of(row_span<kIds>(p, t));
+  for (int t = row0; t < row1; ++t) own += places_of(share_span<kIds, kWalk>(p, t));
   long long incl = own;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -99,7 +114,7 @@ __device__ __forceinline__ Share find_share(const AttentionParams& p, int units,
   if (x0 == x1 && threadIdx.x == 0) share = Share{0, 0, 0, 0, (int)per};
   if (x0 < x1 && before * units <= x0 && x0 < (before + own) * units) {
     for (int t = row0;; ++t) {
-      const int n = places_of(row_span<kIds>(p, t));
+      const int n = places_of(share_span<kIds, kWalk>(p, t));
       if (x0 < (before + n) * units) {
         const int unit = (int)((x0 - before * units) / n);
         share = Share{t, unit, (int)(x0 - before * units - (long long)unit * n), (int)(x1 - x0),
@@ -113,7 +128,7 @@ __device__ __forceinline__ Share find_share(const AttentionParams& p, int units,
   return share;
 }
 
-template <int D, int NT, bool kIds, bool kTeam>
+template <int D, int NT, bool kIds, int kWalk>
 __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>::kPerSm)
     attention_shares_kernel(const __grid_constant__ AttentionParams p) {
   using Shape = ShareShape<D, NT>;
@@ -122,18 +137,20 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
   const int groups = (p.c.heads + p.together - 1) / p.together;
-  const int of = Shape::kWarps / p.together;  // warps of a head
+  const int of = Shape::kWarps / (kWalk >= kByPages ? kWalk : p.together);  // warps of a head
   // this warp's head of the group and its turn; the warps of a team have
   // neighbouring heads and the same turn
-  constexpr int kMembers = kTeam ? Shape::kTeam : 1;
+  constexpr int kMembers = kWalk == kByTeam ? Shape::kTeam : 1;
   const int rest = warp / kMembers;
   const int head = rest / of * kMembers + warp % kMembers, sub = rest % of;
+  if constexpr (kWalk >= kByPages) begin_pages<D, kWalk>(smem);
+  PageState state;
   grid_dependency_wait();
-  Share s = find_share<kIds, Shape::kWarps>(p, groups * p.head_tiles, of);
+  Share s = find_share<kIds, kWalk, Shape::kWarps>(p, groups * p.head_tiles, of);
 
   int4 record = make_int4(0, 0, 0, 0);
   while (s.left > 0) {
-    const RowSpan r = row_span<kIds>(p, s.t);
+    const RowSpan r = share_span<kIds, kWalk>(p, s.t);
     // this share's places of the unit: [s.at, to), tile i at kPieceTiles + i
     const int places = places_of(r), to = min(places - s.at, s.left) + s.at;
     const int tiles = places - kPieceTiles;
@@ -144,7 +161,10 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
     const int heads = active ? min(8 * NT, p.group - ht * 8 * NT) : 0;  // query heads
     const int head0 = h * p.group + ht * 8 * NT;
     Heads<D, NT> hd;
-    if constexpr (kTeam)
+    if constexpr (kWalk >= kByPages)
+      attend_pages<D, NT, kWalk>(p, r, s.t, head, head0, heads, tile0, tile1, sub, smem, state,
+                                 hd);
+    else if constexpr (kWalk == kByTeam)
       attend_team<D, NT, kIds>(p, r, s.t, h - warp % kMembers,
                                min(kMembers, p.c.heads - (h - warp % kMembers)), warp % kMembers,
                                active, head0, heads, tile0, tile1, sub, of, smem, hd);
@@ -192,6 +212,8 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
                   hd.o[n][i][e] * mine[e & 1] + w[(4 + 4 * i + e) * 32] * theirs[e & 1];
         }
       }
+      // bulk copies come here next
+      if constexpr (kWalk >= kByPages) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
     }
 

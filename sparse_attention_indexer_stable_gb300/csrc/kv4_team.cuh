@@ -48,6 +48,10 @@ template <int D>
 struct TeamAt {
   using S = TeamStage<D>;
   const uint8_t *k0, *v0, *ks0, *vs0;
+  static constexpr int kSubStep = 16, kHalfStep = 8;  // tokens
+  static constexpr bool kRaw = false;
+  __device__ void k_read() const {}
+  __device__ void v_wait() const {}
 
   static __device__ __forceinline__ constexpr int token(int i) { return RingAt<D>::token(i); }
   __device__ TeamAt(const uint8_t* stage, int head, int g, int tq) {

@@ -50,6 +50,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "bulk_copy.cuh"
 #include "topk_core.cuh"
 
 namespace dcp {
@@ -62,7 +63,6 @@ constexpr uint32_t kNegInfKey = 0x007FFFFFu;  // score key of -inf: padding's, w
 constexpr uint32_t kBigBucket = 255;          // a larger bucket starting before K sends the row to the fallback
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr unsigned long long kStageWaitLimit = 1ull << 31;  // cycles (about 1 s) to wait for a row's copy
-constexpr uint32_t kStatusCopyTimeout = 1u;     // device status bit: a staging copy timed out
 constexpr uint32_t kStatusBadShardAlignment = 2u;  // device status bit: a shard not 16-byte aligned
 
 // Per-row sizes for a CTA of NT threads selecting up to KMAX winners.
@@ -147,46 +147,6 @@ static_assert(stream_caps_ok<512, kStreamMaxK>(), "caps");
 static_assert(stream_caps_ok<1024, kStreamMaxK>(), "caps");
 static_assert(stream_caps_ok<1024, kStreamMaxKWide>(), "caps");
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-// mbarrier and 1-D bulk-copy (TMA) primitives.  One thread arms the barrier
-// with the byte count of a row and issues the row's copies; every thread then
-// waits on the barrier's phase.
-__device__ __forceinline__ void mbar_init(unsigned long long* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(count)
-               : "memory");
-}
-__device__ __forceinline__ void mbar_fence_init() {
-  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(unsigned long long* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(unsigned long long* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0u;
-}
-// Copies `bytes` (a multiple of 16; both addresses 16-byte aligned) from
-// global to shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_1d(void* smem_dst, const void* gmem_src, uint32_t bytes,
-                                            unsigned long long* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-          smem_u32(smem_dst)),
-      "l"(gmem_src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Marks the rows t, t + G, ... < T of a CTA that stops after a copy timed
 // out: every slot gets id DCP_ID_UNWRITTEN and a NaN score, so that a
 // caller who does not check the device status cannot mistake stale memory
@@ -201,18 +161,6 @@ __device__ __forceinline__ void mark_rows_unwritten(float* out_scores, int32_t* 
       oi[j] = INT32_MIN;                      // DCP_ID_UNWRITTEN
     }
   }
-}
-
-// Waits for phase `parity` of `bar` to complete, giving up once `limit`
-// SM clock cycles have passed (each poll returns within a bounded time, so
-// the wait is bounded).  Returns whether the phase completed.
-__device__ __forceinline__ bool mbar_wait_bounded(unsigned long long* bar, uint32_t parity,
-                                                  unsigned long long limit) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = clock64();
-  while (clock64() - t0 < limit)
-    if (mbar_try_wait(bar, parity)) return true;
-  return false;
 }
 
 // Programmatic dependent launch: wait until the stream's previous grid has

@@ -287,6 +287,42 @@ def test_even_shares_of_all_head_counts(dk, heads, dim, group, with_ids):
     assert np.all(np.abs(w.double().cpu().numpy() - want) <= tol + 2.0 ** -23 * want)
 
 
+@pytest.mark.parametrize("heads,dim,group,page", [
+    (8, 128, 8, 64), (8, 128, 1, 8), (8, 128, 20, 16), (8, 64, 3, 16), (8, 64, 9, 32),
+    (8, 256, 2, 8), (4, 128, 8, 128), (4, 128, 12, 16), (4, 256, 5, 32), (8, 128, 2, 4)])
+def test_even_shares_by_runs_of_a_page(dk, heads, dim, group, page):
+    """All heads of 8 tokens copied at once: windows that begin anywhere, NaN
+    scales in every slot that no row sees, holes, lengths that are no row's."""
+    rng = np.random.default_rng(heads + dim + group + page)
+    rows, pages, width = 7, 640 // page * 7, 48000 // page
+    cache, host = fill(dk, rng, pages, page, heads, dim)
+    table = np.full((rows, width), -1)
+    table[:, :640 // page] = rng.permutation(pages).reshape(rows, -1)
+    hole = 320 // page
+    table[0, hole], table[2, hole:hole + 2] = -1, [pages, 2 ** 30]
+    lens, starts = np.array([640, 0, 637, 33, 1, 500, -3]), np.array([5, 0, 131, 32, 0, 483, 0])
+    pos = np.arange(width * page)
+    for t in range(rows):  # poison what the row does not see
+        unseen = np.flatnonzero((pos[:640] < starts[t]) | (pos[:640] >= lens[t]))
+        slots = table[t, unseen // page] * page + unseen % page
+        slots = slots[(slots >= 0) & (slots < pages * page)]
+        for name in ("k_scales", "v_scales", "k_codes", "v_codes"):
+            getattr(cache, name).view(pages * page, heads, -1)[torch.from_numpy(slots).to(DEV)] = 255
+    q, values = query(rng, rows, heads * group, dim, "bf16")
+    assert dk.kv4_attention_workspace_size(cache, rows, heads * group, width) > 0
+    for softcap in (0.0, 20.0):
+        out, lse = check(dk, cache, host, q, values, "bf16", table, lens, starts=starts,
+                         softcap=softcap)
+    w = torch.zeros(rows, 640, device=DEV)
+    out2, lse2 = dk.kv4_attention(cache, q, i32(table), i32(lens), starts=i32(starts), weights=w,
+                                  softcap=20.0)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    _, _, want, _, _, tol = ref.attention(host, values, table, np.maximum(lens, 0), starts=starts,
+                                          positions=640, softcap=20.0)
+    assert np.all(np.abs(w.double().cpu().numpy() - want) <= tol + 2.0 ** -23 * want)
+    assert dk.dcp_topk_device_status() == 0
+
+
 def test_starts_negative_lengths_and_lengths_beyond_the_table(dk):
     rng = np.random.default_rng(7)
     cache, host = fill(dk, rng, 40, 16, 2, 128)

@@ -10,8 +10,9 @@
 //
 // Measured (8 heads x 128, 8 query heads each): 256 rows of 64 to 8192 tokens
 // 210 us, 5.8 TB/s, 86% of the measured copy rate (see kv4_pages.cuh).  16 rows
-// of 1 to 16384 tokens 38 us, two of 131072 58 us: there 10 us go by before the
-// first tile and after the last, 4 in the join.
+// of 1 to 16384 tokens 38 us, two of 131072 58 us: there 7 go by before the
+// first tile has landed, 3 to 5 between the median CTA's end and the last one's,
+// 4 to 6 in the join.
 //
 // Measured and not taken: one producer warp that copies a token's rows of all
 // heads in bulk (cp.async.bulk, 4 a token): about 60 cycles a copy, 983 us

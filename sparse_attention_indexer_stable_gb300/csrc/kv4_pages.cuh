@@ -183,6 +183,9 @@ __device__ __forceinline__ void attend_pages(const AttentionParams& p, const Row
       reinterpret_cast<uint8_t*>(ring.masks + stage)[run] =
           ok ? (uint8_t)((0xFFu << lo) & (0xFFu >> (8 - hi))) : (uint8_t)0;
     }
+    // lane 0's arrival publishes the others' bytes too; it completes the phase
+    // at once where no run is in the cache
+    __syncwarp();
     if (lane == 0)
       mbar_expect_tx(ring.landed(v, stage),
                      (uint32_t)(__popc(runs) * S::kRun * (S::kCodeRow + S::kScaleRow)));

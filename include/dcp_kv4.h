@@ -146,9 +146,10 @@ dcp_status dcp_kv4_attention_workspace_size(const dcp_kv4_cache* cache,
  * or page size outside the limits, more than 2^31 - 1 positions, or weights of
  * more than 4096 query heads;
  * DCP_ERR_CUDA if a launch fails.  rows == 0 is a no-op.
- * Waits for copies are bounded (about a second): if one never lands,
+ * Waits for copies are bounded: a CTA one of whose copies does not land within
+ * about a second gives up and ends a second later.  Then
  * DCP_DEVICE_COPY_TIMEOUT is set in the device status word
- * (dcp_topk_device_status) and the rows that needed it are NaN.
+ * (dcp_topk_device_status), and the rows that the CTA had not finished are NaN.
  */
 dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention_args* args,
                              dcp_stream_t stream);

@@ -42,8 +42,9 @@ def _inputs():
 
 # The race-check build: the same library compiled with -DDCP_DEBUG_POISON
 # (odd warps delayed after every barrier, shared state overwritten with
-# garbage before every reset, indices from shared state clamped), for the
-# barrier tests only; it exports the same C ABI.
+# garbage before every reset, indices from shared state clamped; the 4-bit
+# cache's waits for copies short, and a copy that it can be told to leave out),
+# for the barrier and time-out tests only; it exports the same C ABI.
 POISON_LIB_PATH = os.path.join(OUT_DIR, "libdcp_topk_racecheck.so")
 POISON_FLAGS = ("-DDCP_DEBUG_POISON",)
 

@@ -58,6 +58,9 @@ static dcp_status planes_of(const dcp_kv4_cache* c, Planes* out) {
 static dcp_status status_of(cudaError_t e) { return e == cudaSuccess ? DCP_OK : DCP_ERR_CUDA; }
 
 // -------------------------------------------------------------- attention
+#ifdef DCP_DEBUG_POISON
+static std::atomic<int> g_withheld[2] = {{-1}, {-1}};  // see dcp_kv4_selftest_withhold
+#endif
 static std::atomic<bool> g_ready[64];
 static unsigned int* g_status[64];  // each device's status word, before g_ready
 static std::mutex g_dev_mutex;
@@ -417,6 +420,9 @@ dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention
   p.score_pairs = a->q_heads % 2 == 0 && p.group % 2 == 0;
   p.scale = (a->scale != 0.0f ? a->scale : 1.0f / sqrtf((float)cache->dim)) * cache->k_unit;
   p.softcap = a->softcap;
+#ifdef DCP_DEBUG_POISON
+  p.withheld_share = g_withheld[0], p.withheld_tile = g_withheld[1];
+#endif
   if (prepare_device(&p.status) != cudaSuccess) return DCP_ERR_CUDA;
   return status_of(launch_all(p, cache->dim, plan, (cudaStream_t)stream));
 }
@@ -469,5 +475,14 @@ dcp_status dcp_kv4_evict(const dcp_kv4_cache* cache, const dcp_kv4_evict_args* a
              (cudaStream_t)stream, p);
   return status_of(e);
 }
+
+#ifdef DCP_DEBUG_POISON
+// Race-check build: from now on attention by runs of a page (kv4_pages.cuh)
+// does not bring in the given tile of the given share (-1: none), so that the
+// waits for it run out, after a limit that is short in this build.
+void dcp_kv4_selftest_withhold(int share, int tile) {
+  g_withheld[0] = share, g_withheld[1] = tile;
+}
+#endif
 
 }  // extern "C"

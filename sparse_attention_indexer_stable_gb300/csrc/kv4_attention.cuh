@@ -75,6 +75,9 @@ struct AttentionParams {
   bool score_pairs;   // two heads' scores can be stored at once
   float scale;        // of q.k, the K unit folded in
   float softcap;      // 0: none
+#ifdef DCP_DEBUG_POISON
+  int withheld_share, withheld_tile;  // see dcp_kv4_selftest_withhold
+#endif
 };
 
 // The tokens a row sees: positions [start, end), or num_ids ids of which

@@ -36,9 +36,10 @@ struct PageStage {
   static constexpr int kHalf = kScales + kRuns * kScaleRun;    // codes, scales
   static constexpr int kBytes = 2 * kHalf;
   static constexpr int kGroups = 8 / kHeads;  // of a CTA
-  // their stages, then K's and V's barriers and the masks
+  // their stages, then K's and V's barriers, the masks, and whether a wait ran out
   static constexpr int kRings = kGroups * kStages * kBytes;
-  static constexpr int kSmem = kRings + kGroups * kStages * (4 * 8 + 4);
+  static constexpr int kGaveUp = kRings + kGroups * kStages * (4 * 8 + 4);
+  static constexpr int kSmem = kGaveUp + 4;
 };
 
 // A group's part of that.
@@ -108,54 +109,84 @@ struct PageAt {
   }
 };
 
-constexpr unsigned long long kPageWaitLimit = 1ull << 31;  // cycles (about 1 s)
+// Cycles that a copy is waited for.  When they have passed, the CTA gives up:
+// its warps bring nothing in any more, wait for nothing any more, and write NaN
+// for what they have not finished; before it ends it lets the same time pass
+// once more, for copies that are still on their way into its shared memory.
+#ifdef DCP_DEBUG_POISON
+constexpr unsigned long long kPageWaitLimit = 1ull << 22;  // about 2 ms
+#else
+constexpr unsigned long long kPageWaitLimit = 1ull << 31;  // about 1 s
+#endif
 
-// What a warp carries from one call to the next: how many tiles its group has
-// walked, and whether a wait ran out.  Then its sums are NaN, it brings nothing
-// in any more and waits for nothing any more.
-struct PageState {
-  uint32_t done = 0;
-  bool failed = false;
-};
+template <int D, int kHeads>
+__device__ __forceinline__ volatile uint32_t* gave_up(uint8_t* smem) {
+  return reinterpret_cast<volatile uint32_t*>(smem + PageStage<D, kHeads>::kGaveUp);
+}
+
+// Waits for phase `parity` of `bar`, the whole warp, with one answer: false if
+// the CTA has given up.
+__device__ __forceinline__ bool page_wait(unsigned long long* bar, uint32_t parity,
+                                          volatile uint32_t* over, unsigned int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = clock64();
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const bool late = clock64() - t0 >= kPageWaitLimit;
+    if (late) {
+      atomicOr(status, kStatusCopyTimeout);
+      *over = 1u;
+    }
+    if (__any_sync(0xffffffffu, late || *over)) return false;
+  }
+}
 
 // A barrier of the CTA has to follow.
 template <int D, int kHeads>
 __device__ __forceinline__ void begin_pages(uint8_t* smem) {
   using S = PageStage<D, kHeads>;
   constexpr int kBars = 4 * S::kStages;  // of a group
+  if (threadIdx.x == 0) *gave_up<D, kHeads>(smem) = 0u;
   if (threadIdx.x < S::kGroups * kBars)
     mbar_init(PageRing<D, kHeads>(0, smem).bars + threadIdx.x,
               threadIdx.x % kBars < 2 * S::kStages ? 1 : kHeads);
   mbar_fence_init();
 }
 
+// The CTA's end.
+template <int D, int kHeads>
+__device__ __forceinline__ void end_pages(uint8_t* smem) {
+  if (!*gave_up<D, kHeads>(smem)) return;
+  const unsigned long long t0 = clock64();
+  while (clock64() - t0 < kPageWaitLimit) {
+  }
+}
+
 // attend_tiles for one of the kHeads warps of a group, this one's head being
-// `head`.  The group's tiles are numbered over all its calls, state.done of them
+// `head`.  The group's tiles are numbered over all its calls, `walked` of them
 // so far; warp n % kHeads brings tile n in.  It does so when it has read tile
 // n - 2 itself, so that the others have had a tile's time to read tile n - 3,
 // whose stage n takes.
 template <int D, int NT, int kHeads>
 __device__ __forceinline__ void attend_pages(const AttentionParams& p, const RowSpan& r, int t,
                                              int head, int head0, int q_heads, int tile0,
-                                             int tile1, int sub, uint8_t* smem, PageState& state,
+                                             int tile1, int sub, uint8_t* smem, uint32_t& walked,
                                              Heads<D, NT>& hd) {
   using S = PageStage<D, kHeads>;
   constexpr int kOf = S::kGroups;
   const PageRing<D, kHeads> ring(sub, smem);
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
-  const int mine = tile1 - tile0 > sub
+  volatile uint32_t* const over = gave_up<D, kHeads>(smem);
+  const int mine = tile1 - tile0 > sub && !__any_sync(0xffffffffu, *over)
                        ? (int)((unsigned)(tile1 - tile0 - sub + kOf - 1) / (unsigned)kOf)
                        : 0;
   hd.fetch(p, t, head0, q_heads);
   const int32_t* table = p.table + (int64_t)r.seq * p.table_stride;
 
-  const uint32_t done = state.done;
+  const uint32_t done = walked;
   auto wait = [&](unsigned long long* bar, uint32_t parity) {
-    if (mbar_wait_bounded(bar, parity, state.failed ? 0ull : kPageWaitLimit)) return;
-    state.failed = true;
-    atomicOr(p.status, kStatusCopyTimeout);
-    mbar_wait_bounded(bar, parity, kPageWaitLimit);  // time for what is still on its way
+    return page_wait(bar, parity, over, p.status);
   };
   // a run's first position (r.start is a multiple of 8) and page
   const int run = lane & 3;
@@ -169,14 +200,17 @@ __device__ __forceinline__ void attend_pages(const AttentionParams& p, const Row
   };
   int next = (int)((uint32_t)(head - (int)done) % (uint32_t)kHeads);  // this warp's next tile
   int page = look(next);
-  // K (v = 0) or V (1) of tile `next`: lanes 0 to 3 copy a run's codes, 4 to 7 its scales
+  // K (v = 0) or V (1) of tile `next`: lanes 0 to 3 copy a run's codes, 4 to 7 its
+  // scales.  False if the CTA has given up.
   auto issue = [&](int v) {
     const uint32_t n = done + (uint32_t)next, stage = n % S::kStages;
-    if (n >= S::kStages) wait(ring.read(v, stage), (n / S::kStages - 1) & 1);
+    if (n >= S::kStages && !wait(ring.read(v, stage), (n / S::kStages - 1) & 1)) return false;
+#ifdef DCP_DEBUG_POISON
+    if ((int)blockIdx.x == p.withheld_share && (int)n == p.withheld_tile) return false;
+#endif
     const uint32_t pos = place(next);
     // the runs that are in the cache, as lanes 0 to 3 see it
-    const uint32_t runs = __ballot_sync(0xffffffffu, (uint32_t)page < p.c.num_pages &&
-                                                         !state.failed) & 0xFu;
+    const uint32_t runs = __ballot_sync(0xffffffffu, (uint32_t)page < p.c.num_pages) & 0xFu;
     const bool ok = (runs >> run) & 1u;
     if (v == 0 && lane < S::kRuns) {
       const int lo = max(0, r.start + r.skip - (int)pos), hi = min(8, r.end - (int)pos);
@@ -206,17 +240,21 @@ __device__ __forceinline__ void attend_pages(const AttentionParams& p, const Row
       next += kHeads;
       page = look(next);
     }
+    return true;
+  };
+  auto bring = [&] {
+    if (issue(0)) issue(1);
   };
 
 #pragma unroll 1
   for (int k = 0; k < S::kStages - 1; ++k)
-    if (k == next && k < mine) issue(0), issue(1);
+    if (k == next && k < mine) bring();
   hd.begin(p, t, head0, q_heads, tile0 == 0 && sub == 0);
 
   uint32_t stage = done % S::kStages, parity = done / S::kStages & 1;
 #pragma unroll 1
   for (int k = 0; k < mine; ++k) {
-    wait(ring.landed(0, stage), parity);
+    if (!wait(ring.landed(0, stage), parity)) break;
     const uint32_t mask = ring.masks[stage];
     auto k_read = [&] {
       __syncwarp();
@@ -229,14 +267,10 @@ __device__ __forceinline__ void attend_pages(const AttentionParams& p, const Row
                        mask, (int64_t)kTile * (tile0 + sub + (int64_t)kOf * k), hd);
     __syncwarp();
     if (lane == 0) mbar_arrive(ring.read(1, stage));
-    if (k + S::kStages - 1 == next && next < mine) issue(0), issue(1);
+    if (k + S::kStages - 1 == next && next < mine) bring();
     if (++stage == S::kStages) stage = 0, parity ^= 1;
   }
-  state.done += mine;
-  if (state.failed) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) hd.l[n][0] = hd.l[n][1] = __int_as_float(0x7fffffff);
-  }
+  walked += mine;
 }
 
 }  // namespace kv4

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
   const int rest = warp / kMembers;
   const int head = rest / of * kMembers + warp % kMembers, sub = rest % of;
   if constexpr (kWalk >= kByPages) begin_pages<D, kWalk>(smem);
-  PageState state;
+  uint32_t walked = 0;  // kByPages: tiles of this warp's group
   grid_dependency_wait();
   Share s = find_share<kIds, kWalk, Shape::kWarps>(p, groups * p.head_tiles, of);
 
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
     const int head0 = h * p.group + ht * 8 * NT;
     Heads<D, NT> hd;
     if constexpr (kWalk >= kByPages)
-      attend_pages<D, NT, kWalk>(p, r, s.t, head, head0, heads, tile0, tile1, sub, smem, state,
+      attend_pages<D, NT, kWalk>(p, r, s.t, head, head0, heads, tile0, tile1, sub, smem, walked,
                                  hd);
     else if constexpr (kWalk == kByTeam)
       attend_team<D, NT, kIds>(p, r, s.t, h - warp % kMembers,
@@ -174,10 +174,10 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
                                 active ? tile1 : tile0, sub, of, smem, hd);
 
     // the warps of a head add up in halves, in the ring's place
-    float* state = reinterpret_cast<float*>(smem);
+    float* sums = reinterpret_cast<float*>(smem);
     if (of > 1) __syncthreads();  // every warp has read its ring
     for (int step = of >> 1; step > 0; step >>= 1) {
-      float* slot = state + (head * step + sub % step) * kStateWords * 32 + lane;
+      float* slot = sums + (head * step + sub % step) * kStateWords * 32 + lane;
       if (sub >= step && sub < 2 * step) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -226,11 +226,14 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
         p.cuts[(int64_t)s.t * groups * p.head_tiles + s.unit] = make_int2((int)blockIdx.x, last);
     }
     if (sub == 0) {
+      // what the CTA gave up on; late copies may have hit the warps' sums, too
+      bool lost = false;
+      if constexpr (kWalk >= kByPages) lost = *gave_up<D, kWalk>(smem);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float sum = hd.l[n][c];
+          float sum = lost ? __int_as_float(0x7fffffff) : hd.l[n][c];
           sum += __shfl_xor_sync(0xffffffffu, sum, 4);
           sum += __shfl_xor_sync(0xffffffffu, sum, 8);
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(ShareShape<D, NT>::kThreads, ShareShape<D, NT>
     if (++s.unit == groups * p.head_tiles) s.unit = 0, ++s.t;
   }
   if (threadIdx.x == 0) p.shares[blockIdx.x] = record;
+  if constexpr (kWalk >= kByPages) end_pages<D, kWalk>(smem);
 }
 
 // Joins the pieces of a unit that shares cut.  kByUnit: a CTA per unit and

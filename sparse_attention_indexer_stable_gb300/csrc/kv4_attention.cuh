@@ -3,8 +3,8 @@
 // For one row and one key/value head, with the group's query heads q_h and
 // the visible tokens j:
 //   x_hj = c(q_h . k_j) in units of log2,  out_h = sum_j 2^(x_hj - m_h) v_j / l_h
-// with m_h a reference within 2^8 of the running maximum and l_h the running
-// sum.  A token costs dim + dim/8 bytes and 4 * dim operations per query
+// with m_h a reference from 2^7 below the running maximum to 2^15 below it and
+// l_h the running sum.  A token costs dim + dim/8 bytes and 4 * dim operations per query
 // head, so with up to 16 heads to a group the cache's bytes bound it, closely
 // followed by the conversions of its codes.
 //
@@ -22,7 +22,11 @@
 //  - P moves from the accumulator's layout to the operand's by one transpose
 //    of 8x8 matrices per 8 tokens (movmatrix).
 //  - The accumulator is rescaled only when a score passes the reference by
-//    2^8 (fp16 holds P up to 65504), which after the first tiles is rare.
+//    2^15 (fp16 holds P up to 65504), which after the first tiles is rare: the
+//    reference is set 2^7 below the maximum.  That also keeps light tokens: P
+//    in fp16 steps by 2^-24 at the least, 2^-31 or less of the heaviest token's.
+//    With the reference at the maximum, 2^17 tokens of 2^-25 each, a third of a
+//    percent of a row together, fell out of the products and stayed in the sum.
 //
 // Two kernels cut a call up: kv4_slices.cuh for short rows, kv4_shares.cuh for
 // long rows and rows of different lengths; kv4_ring.cuh brings the tiles in.
@@ -36,7 +40,8 @@ namespace dcp {
 namespace kv4 {
 
 constexpr float kNoScore = -3.0e38f;  // reference of a head that has seen no token
-constexpr float kSlack = 8.0f;        // scores may pass the reference by 2^8
+constexpr float kBelow = 7.0f;        // a reference is set 2^7 below the maximum
+constexpr float kSlack = 15.0f;       // and scores may pass it by 2^15
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTile = 32;  // tokens of a tile: one per lane to look up
@@ -469,7 +474,7 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
       for (int e = c + 2; e < 4 * kSub; e += 2)
         top[n][c] = fmaxf(top[n][c], s[n][e >> 2][e & 3]);
       top[n][c] *= hd.late[n][c];
-      past |= top[n][c] > hd.m[n][c] + kSlack;
+      past |= top[n][c] - hd.m[n][c] > kSlack;  // as a difference: exact where both are large
     }
   if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
@@ -480,7 +485,7 @@ __device__ __forceinline__ void attend_tile(const AttentionParams& p, const RowS
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        const float mn = fmaxf(hd.m[n][c], x);
+        const float mn = fmaxf(hd.m[n][c], x - kBelow);
         const float corr = exp2_approx(hd.m[n][c] - mn);
         hd.m[n][c] = mn;
         hd.l[n][c] *= corr;

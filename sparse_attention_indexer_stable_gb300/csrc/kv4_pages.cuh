@@ -271,6 +271,7 @@ __device__ __forceinline__ void attend_pages(const AttentionParams& p, const Row
     if (++stage == S::kStages) stage = 0, parity ^= 1;
   }
   walked += mine;
+  hd.end();
 }
 
 }  // namespace kv4

@@ -176,6 +176,7 @@ __device__ __forceinline__ void attend_tiles(const AttentionParams& p, const Row
     attend_tile<D, NT>(p, r, t, head0, heads, RingAt<D>(st, g, tq), mask,
                        (int64_t)kTile * (tile0 + sub + (int64_t)of * k), hd);
   }
+  hd.end();
   cp_async_wait<0>();
 }
 

@@ -185,6 +185,7 @@ __device__ __forceinline__ void attend_team(const AttentionParams& p, const RowS
       attend_tile<D, NT>(p, r, t, head0, heads, TeamAt<D>(st, member, g, tq), mask,
                          (int64_t)kTile * (tile0 + sub + (int64_t)of * k), hd);
   }
+  hd.end();
   cp_async_wait<0>();
 }
 

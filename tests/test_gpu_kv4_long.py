@@ -31,7 +31,7 @@ def test_one_heavy_token_among_many_light_ones(dk, with_ids):  # noqa: F811
     first = 23.296875
     q = torch.randn(rows, heads, dim, generator=gen, device=DEV).half()
     q[:, :, 0] = first
-    out, _ = dk.kv4_attention(cache, q, table.expand(rows, -1), i32([n] * rows),
+    out, lse = dk.kv4_attention(cache, q, table.expand(rows, -1), i32([n] * rows),
                                 ids=order.expand(rows, -1) if with_ids else None)
     score = 6 * first * dim ** -0.5
     want_lse = score + math.log1p((n - 1) * math.exp(-score))
@@ -42,3 +42,5 @@ def test_one_heavy_token_among_many_light_ones(dk, with_ids):  # noqa: F811
     # ones' to fp16's smallest step below a reference of 2^7, and fp32's
     tol = 3 * (2.0 ** -11 + n * 2.0 ** -32 + 2.0 ** -18) + 2.0 ** -11 * abs(want)
     assert np.abs(out.double().cpu().numpy() - want).max() <= tol
+    # light tokens beside a heavy one in a lane's running sum count, too
+    assert np.abs(lse.double().cpu().numpy() - want_lse).max() <= 2.0 ** -18

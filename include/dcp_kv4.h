@@ -140,8 +140,9 @@ dcp_status dcp_kv4_attention_workspace_size(const dcp_kv4_cache* cache,
                                             const dcp_kv4_attention_args* args, size_t* bytes);
 
 /*
- * Errors: DCP_ERR_INVALID for a bad cache or dtype, negative sizes, q_heads
- * not a multiple of heads, a NULL required pointer with rows > 0, weights with
+ * Errors: DCP_ERR_INVALID for a bad cache or dtype, negative sizes, a softcap
+ * that is negative, a softcap or scale that is not finite, q_heads not a
+ * multiple of heads, a NULL required pointer with rows > 0, weights with
  * owner, or a workspace smaller than reported; DCP_ERR_UNSUPPORTED for a dim
  * or page size outside the limits, more than 2^31 - 1 positions, or weights of
  * more than 4096 query heads;

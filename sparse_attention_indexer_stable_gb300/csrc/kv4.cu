@@ -145,8 +145,8 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
                           const dcp_kv4_attention_args* a, Plan* plan) {
   if (!a || (a->dtype != DCP_F16 && a->dtype != DCP_BF16) || a->rows < 0 || a->q_heads < 1 ||
       a->q_heads % c->heads || a->num_seqs < 0 || a->table_width < 0 || a->max_len < 0 ||
-      (a->ids && a->num_ids < 0) || (a->weights && a->owner) || !(a->softcap >= 0.0f) ||
-      a->weights_width < 0)
+      (a->ids && a->num_ids < 0) || (a->weights && a->owner) || !std::isfinite(a->scale) ||
+      !std::isfinite(a->softcap) || a->softcap < 0.0f || a->weights_width < 0)
     return DCP_ERR_INVALID;
   const int64_t capacity = (int64_t)a->table_width << planes.page_shift;
   if (capacity > INT_MAX) return DCP_ERR_UNSUPPORTED;

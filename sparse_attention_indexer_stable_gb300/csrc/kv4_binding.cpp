@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <optional>
 #include <string>
 
@@ -265,8 +266,10 @@ PyObject* attention(PyObject*, PyObject* const* p, Py_ssize_t n) {
     if (!owner && table.size(0) < T)
       value_error("table must have a row for each row of q (or give owner)");
     a.softcap = float_of(p[10]);
-    if (!(a.softcap >= 0.0f)) value_error("softcap must not be negative");
+    if (!std::isfinite(a.softcap) || a.softcap < 0.0f)
+      value_error("softcap must be finite and not negative");
     a.scale = p[9] == Py_None ? 0.0f : float_of(p[9]);
+    if (!std::isfinite(a.scale)) value_error("scale must be finite");
     a.q = q.data_ptr();
     a.q_row_stride = q.stride(0);
     a.q_head_stride = q.stride(1);

@@ -329,8 +329,9 @@ struct Heads {
       const float undo = convert_query<D>(p, qf[n]) * unit;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        // above 0: -infinity times it stays -infinity
-        mult[n][c] = fmaxf(__shfl_sync(0xffffffffu, undo, 8 * tq + 4 * c), 1e-37f);
+        // above 0: -infinity times it stays -infinity; finite: 0 times it stays 0
+        mult[n][c] =
+            fminf(fmaxf(__shfl_sync(0xffffffffu, undo, 8 * tq + 4 * c), 1e-37f), 3e38f);
         late[n][c] = capped ? 1.0f : mult[n][c];
         const int head = 8 * n + 2 * tq + c;
         if (write_mult && p.row_mult && g == 0 && head < heads)

@@ -1,4 +1,6 @@
 """Edges of the 4-bit cache's operators on the GPU."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -15,3 +17,17 @@ def test_a_scale_or_cap_that_is_not_finite_is_refused(dk, name):  # noqa: F811
     for value in (float("inf"), -float("inf"), float("nan"), 1e39):  # the last: no float
         with pytest.raises(ValueError, match=name):
             dk.kv4_attention(cache, q, i32([[0]]), i32([1]), **{name: value})
+
+
+@pytest.mark.parametrize("q_size,key,named", [
+    (3e38, 0.0, dict(scale=1e6)),       # products of 0 with what is beyond fp32
+    (1.0, 0.0, dict(softcap=1e-44)),
+    (1.0, 3.0, dict(softcap=1e-44))])   # every score at the cap
+def test_equal_scores_whose_multiplier_leaves_fp32(dk, q_size, key, named):  # noqa: F811
+    cache = dk.Kv4Cache.allocate(4, 16, 1, 64, DEV)
+    x = torch.ones(64, 1, 64, device=DEV)
+    dk.kv4_append(cache, key * x, 3 * x, torch.arange(64, device=DEV))
+    q = torch.full((1, 4, 64), q_size, device=DEV).bfloat16()
+    out, lse = dk.kv4_attention(cache, q, i32([[0, 1, 2, 3]]), i32([50]), **named)
+    assert (out == 3).all()  # the mean of equal values: 3 / 6 and 6 are exact
+    assert (lse - math.log(50)).abs().max() <= 2.0 ** -20

@@ -689,6 +689,11 @@ __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ At
       const int given = kIds ? __ldg(p.ids + (int64_t)t * p.ids_stride + j) : (int)j;
       const int pos = token_pos<kIds>(r, row_start, given);
       if (pos >= 0 && pos < p.weights_width) {
+        // a head whose sum is NaN made the absent tokens' shares NaN, too
+        if (sum[i] != sum[i] &&
+            (uint32_t)__ldg(p.table + (int64_t)r.seq * p.table_stride +
+                            (pos >> p.c.page_shift)) >= p.c.num_pages)
+          continue;
         float* w = p.weights + (int64_t)t * p.weights_stride + pos;
         if constexpr (kIds)
           atomicAdd(w, sum[i]);  // an id may be listed twice

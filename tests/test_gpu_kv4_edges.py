@@ -31,3 +31,21 @@ def test_equal_scores_whose_multiplier_leaves_fp32(dk, q_size, key, named):  # n
     out, lse = dk.kv4_attention(cache, q, i32([[0, 1, 2, 3]]), i32([50]), **named)
     assert (out == 3).all()  # the mean of equal values: 3 / 6 and 6 are exact
     assert (lse - math.log(50)).abs().max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("with_ids", [False, True])
+@pytest.mark.parametrize("q_heads", [3, 4])
+def test_weights_of_a_nan_head_stay_with_tokens_that_are_there(dk, q_heads, with_ids):  # noqa: F811
+    cache = dk.Kv4Cache.allocate(4, 16, 1, 64, DEV)
+    x = torch.ones(64, 1, 64, device=DEV)
+    dk.kv4_append(cache, x, x, torch.arange(64, device=DEV))
+    q = torch.ones(2, q_heads, 64, dtype=torch.bfloat16, device=DEV)
+    q[0, 1, 7] = float("nan")
+    w = torch.zeros(2, 60, device=DEV)
+    table = i32([[0, -1, 2, 4], [3, 99, 1, 0]])  # positions 16..31 are holes, row 0's 48..63, too
+    ids = i32([list(range(60)) + [-1] * 9] * 2) if with_ids else None
+    dk.kv4_attention(cache, q, table, i32([60, 40]), ids=ids, starts=i32([4, 0]), weights=w)
+    there = torch.tensor([4 <= p < 16 or 32 <= p < 48 for p in range(60)], device=DEV)
+    assert torch.isnan(w[0, there]).all() and not w[0, ~there].any()
+    assert (w[1, :16] > 0).all() and (w[1, 32:40] > 0).all()
+    assert not w[1, 16:32].any() and not w[1, 40:].any()

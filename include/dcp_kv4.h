@@ -162,8 +162,10 @@ dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention
  * keeps its first `sinks` and last `recent` positions and, of the others, the
  * budget - sinks - recent with the largest weights (equal weights: the lowest
  * position; NaN ranks below everything).  Kept tokens move in their order to
- * positions 0, 1, ... of out_table.  The source pages are left as they are;
- * the pages of out_table must not be among them.
+ * positions 0, 1, ... of out_table.  A kept token on a hole of table becomes
+ * zeros, as it reads; what falls on a hole of out_table is not written.  The
+ * source pages are left as they are; the pages of out_table must not be among
+ * them.
  */
 typedef struct {
     const int32_t* table;      /* [num_seqs][table_width] */

@@ -280,18 +280,18 @@ __global__ void __launch_bounds__(kSelThreads, 1)
 
 constexpr int kCopy = 4;  // tokens of a warp
 
-// Rows of the K and V planes of one kind (those that are live), all loads
-// before the stores.
+// Rows of the K and V planes of one kind (those that are live; zeros for a
+// source that is not there), all loads before the stores.
 template <typename Piece>
 __device__ __forceinline__ void copy_rows(uint8_t* k_plane, uint8_t* v_plane,
                                           const uint64_t (&dst)[kCopy],
-                                          const uint64_t (&src)[kCopy], unsigned live, int bytes,
-                                          int lane) {
+                                          const uint64_t (&src)[kCopy], unsigned live,
+                                          unsigned there, int bytes, int lane) {
   for (int i = lane; i < bytes / (int)sizeof(Piece); i += 32) {
-    Piece x[kCopy], y[kCopy];
+    Piece x[kCopy] = {}, y[kCopy] = {};
 #pragma unroll
     for (int k = 0; k < kCopy; ++k)
-      if ((live >> k) & 1u) {
+      if ((there >> k) & 1u) {
         x[k] = reinterpret_cast<const Piece*>(k_plane + src[k] * (uint64_t)bytes)[i];
         y[k] = reinterpret_cast<const Piece*>(v_plane + src[k] * (uint64_t)bytes)[i];
       }
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
   grid_dependency_wait();
   // the first lanes look a token up each
   uint64_t from = 0, to = 0;
-  bool ok = false;
+  bool ok = false, found = false;
   if (lane < kCopy && item0 + lane < items) {
     const int64_t item = item0 + lane;
     const int pos = p.kept[item];
@@ -321,12 +321,14 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
       const uint32_t page = (uint32_t)__ldg(p.table + (int64_t)b * p.table_stride + (pos >> shift));
       const uint32_t out = (uint32_t)__ldg(p.out_table + (int64_t)b * p.out_table_stride +
                                            (j >> shift));
-      ok = page < p.c.num_pages && out < p.c.num_pages;  // else a hole
+      ok = out < p.c.num_pages;  // else a hole
+      found = ok && page < p.c.num_pages;  // a hole's token reads as zeros
       from = ((uint64_t)page << shift) | (uint32_t)(pos & low);
       to = ((uint64_t)out << shift) | (uint32_t)(j & low);
     }
   }
   const unsigned live = __ballot_sync(0xffffffffu, ok);
+  const unsigned there = __ballot_sync(0xffffffffu, found);
   if (!live) return;
   uint64_t src[kCopy], dst[kCopy];
 #pragma unroll
@@ -334,8 +336,9 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
     src[k] = __shfl_sync(0xffffffffu, from, k);
     dst[k] = __shfl_sync(0xffffffffu, to, k);
   }
-  copy_rows<uint32_t>(p.c.k_scales, p.c.v_scales, dst, src, live, p.row_scales, lane);
-  copy_rows<uint4>(p.c.k_codes, p.c.v_codes, dst, src, live, p.row_codes, lane);
+  copy_rows<uint32_t>(p.c.k_scales, p.c.v_scales, dst, src, live, there, p.row_scales,
+                      lane);
+  copy_rows<uint4>(p.c.k_codes, p.c.v_codes, dst, src, live, there, p.row_codes, lane);
 }
 
 }  // namespace kv4

@@ -49,3 +49,22 @@ def test_weights_of_a_nan_head_stay_with_tokens_that_are_there(dk, q_heads, with
     assert torch.isnan(w[0, there]).all() and not w[0, ~there].any()
     assert (w[1, :16] > 0).all() and (w[1, 32:40] > 0).all()
     assert not w[1, 16:32].any() and not w[1, 40:].any()
+
+
+def test_eviction_leaves_nothing_old_where_a_hole_was_kept(dk):  # noqa: F811
+    """The pages that an eviction fills may hold another sequence's tokens."""
+    cache = dk.Kv4Cache.allocate(8, 4, 2, 64, DEV)
+    planes = cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales
+    for i, plane in enumerate(planes):
+        plane.fill_(17 + i)
+        plane[6:] = 51 + i
+    w = torch.arange(24, dtype=torch.float32, device=DEV).view(2, 12)
+    kept, lens, _ = dk.kv4_evict(cache, i32([[0, -1, 2], [3, 4, 8]]), i32([12, 12]), w,
+                                 i32([[6], [7]]), 4, sinks=1, recent=1)
+    assert kept.tolist() == [[0, 9, 10, 11], [0, 9, 10, 11]]
+    kept2, _, _ = dk.kv4_evict(cache, i32([[-1, 1, 2]]), i32([4]), w[:1], i32([[5]]), 4)
+    assert kept2.tolist() == [[0, 1, 2, 3]]
+    for i, plane in enumerate(planes):
+        assert (plane[6] == 17 + i).all()
+        assert (plane[7, 0] == 17 + i).all() and not plane[7, 1:].any()
+        assert not plane[5].any() and (plane[:5] == 17 + i).all()

@@ -160,6 +160,11 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   // shares by three quarters of it where rows may differ.
   const int64_t units = (int64_t)a->rows * c->heads * plan->head_tiles;
   const int64_t tiles = ((int64_t)plan->width + kTile - 1) / kTile;
+  // before anything is multiplied by more: units <= rows * query heads, so
+  // units * tiles * dim then stays below 2^63
+  if ((int64_t)a->rows * a->q_heads > INT_MAX || units * 8 > INT_MAX ||
+      units * (tiles + kPieceTiles + 2) / kPlanSms > INT_MAX)
+    return DCP_ERR_UNSUPPORTED;
   const int64_t warps = c->dim * plan->heads_per_cta >= 2048 ? 8 : 16;  // of an SM
   auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   // Slices of ids in teams (kv4_team.cuh) where there are whole teams and an SM
@@ -192,9 +197,6 @@ static dcp_status plan_of(const dcp_kv4_cache* c, const Planes& planes,
   // for each warp of a CTA, a CTA joins one head, otherwise a warp does.
   const int64_t cuts = a->rows * ceil_div(c->heads, plan->together) * plan->head_tiles;
   plan->cuts = cuts * 16 <= plan->shares ? (int)cuts : 0;
-  if (units * 8 > INT_MAX || units * (tiles + kPieceTiles + 2) / kPlanSms > INT_MAX ||
-      (int64_t)a->rows * a->q_heads > INT_MAX)
-    return DCP_ERR_UNSUPPORTED;
   const size_t heads = (size_t)a->rows * a->q_heads;
   size_t at = 0;
   auto take = [&at](size_t bytes) {

@@ -16,3 +16,19 @@ def test_a_scale_or_cap_that_is_not_finite_is_refused(name, value):
     n = ctypes.c_size_t(7)
     assert dk.library().dcp_kv4_attention_workspace_size(
         cache(), args, ctypes.byref(n)) == dk.DCP_ERR_INVALID
+
+
+@pytest.mark.parametrize("with_ids", [False, True])
+@pytest.mark.parametrize("heads,group,rows,width", [
+    (65536, 1, 2 ** 31 - 1, 2 ** 22), (65536, 16384, 2 ** 20, 2 ** 22), (1, 1, 2 ** 31 - 1, 2 ** 23),
+    (65536, 32767, 2 ** 31 - 1, 1), (2, 4, 2 ** 28, 2 ** 23 - 1)])
+def test_sizes_whose_products_pass_64_bits_are_refused(heads, group, rows, width, with_ids):
+    """Refused before they are multiplied any further (a build with the
+    compiler's overflow checks reports nothing)."""
+    c = cache(heads=heads, dim=256, page=256, pages=8)
+    n = ctypes.c_size_t(7)
+    args = attention(rows=rows, num_seqs=rows, q_heads=heads * group, table_width=width,
+                     ids=16 if with_ids else 0, num_ids=2 ** 31 - 1 if with_ids else 0)
+    assert dk.library().dcp_kv4_attention_workspace_size(
+        c, args, ctypes.byref(n)) == dk.DCP_ERR_UNSUPPORTED
+    assert n.value == 7

@@ -6,7 +6,6 @@ architecture-specific flags so the same source builds on x86_64 and aarch64.
 """
 from __future__ import annotations
 
-import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -75,10 +74,13 @@ def build_race_check(force: bool = False) -> str:
     return build(force, POISON_FLAGS, POISON_LIB_PATH)
 
 
-# The torch side of the 4-bit cache's functions: host C++ against torch's
-# headers, so built anew for another torch.
+# The torch side of the 4-bit cache's functions: host C++ against torch's and
+# Python's headers, so built anew for another torch, its CUDA, or another Python.
 def binding_path() -> str:
-    return os.path.join(OUT_DIR, f"_kv4_binding-{importlib.metadata.version('torch')}.so")
+    import torch
+
+    return os.path.join(OUT_DIR, f"_kv4_binding-{torch.__version__}-cuda{torch.version.cuda}"
+                                 f"{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def build_binding(force: bool = False) -> str:

@@ -1,9 +1,11 @@
 """Host-side edges of the 4-bit cache's C ABI; no GPU needed."""
 import ctypes
+import sysconfig
 
 import pytest
 
 import sparse_attention_indexer_stable_gb300 as dk
+from sparse_attention_indexer_stable_gb300 import _build
 
 from .test_kv4_capi import attention, cache
 
@@ -32,3 +34,22 @@ def test_sizes_whose_products_pass_64_bits_are_refused(heads, group, rows, width
     assert dk.library().dcp_kv4_attention_workspace_size(
         c, args, ctypes.byref(n)) == dk.DCP_ERR_UNSUPPORTED
     assert n.value == 7
+
+
+def test_the_binding_is_built_for_one_python_and_one_torch(monkeypatch):
+    """Another Python, torch or CUDA of torch: another file, not one of the
+    wrong ABI."""
+    torch = pytest.importorskip("torch")
+    paths = {_build.binding_path()}
+    with monkeypatch.context() as m:
+        real = sysconfig.get_config_var
+        m.setattr(sysconfig, "get_config_var",
+                  lambda name: ".cpython-399-none.so" if name == "EXT_SUFFIX" else real(name))
+        paths.add(_build.binding_path())
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "1.0")
+        paths.add(_build.binding_path())
+    with monkeypatch.context() as m:
+        m.setattr(torch.version, "cuda", "1.0")
+        paths.add(_build.binding_path())
+    assert len(paths) == 4 and all(p.endswith(".so") for p in paths)

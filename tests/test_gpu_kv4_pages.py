@@ -51,3 +51,33 @@ def test_tiles_without_tokens_between_others(dk, heads, dim, group, page, rows):
     again = dk.kv4_attention(cache, q, i32(table), i32(lens))
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
     assert dk.dcp_topk_device_status() == 0
+
+
+@pytest.mark.parametrize("heads,dim,group,page,rows,dtype", [
+    (8, 64, 1, 16, 300, "bf16"), (8, 64, 9, 8, 300, "f16"), (8, 64, 17, 64, 160, "bf16"),
+    (8, 128, 2, 16, 300, "bf16"), (8, 128, 17, 32, 160, "f16"), (8, 256, 1, 128, 160, "f16"),
+    (4, 128, 8, 16, 400, "f16"), (4, 128, 19, 8, 200, "bf16"), (4, 256, 9, 64, 160, "bf16")])
+def test_walks_of_many_tiles(dk, heads, dim, group, page, rows, dtype):  # noqa: F811
+    """Shares of ten places and more, pieces that begin and end anywhere, rows of
+    nothing, windows; the same with weights."""
+    rng = np.random.default_rng(heads * dim + group)
+    cache, host = fill(dk, rng, 64, page, heads, dim)
+    table, lens = walk(rng, 64, page, rows, 1536, rows // 8)
+    starts = np.where(rng.random(rows) < 0.3, rng.integers(0, 1536, rows), 0)
+    q, values = query(rng, rows, heads * group, dim, dtype)
+    assert tiles_of_a_group(heads, dim, group, np.maximum(lens - starts, 0)) * (8 // heads) >= 10
+    assert dk.kv4_attention_workspace_size(cache, rows, heads * group, table.shape[1]) > 0
+    out, lse = check(dk, cache, host, q, values, dtype, table, lens, starts=starts)
+    again = dk.kv4_attention(cache, q, i32(table), i32(lens), starts=i32(starts))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    w = torch.zeros(rows, 1536, device="cuda")
+    out2, lse2 = dk.kv4_attention(cache, q, i32(table), i32(lens), starts=i32(starts), weights=w)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    # a row's weights sum to its query heads, each head's to 1 within the fp32
+    # sums of 1536 tokens, and lie inside its window
+    pos = torch.arange(1536, device="cuda")
+    seen = (pos >= i32(starts)[:, None]) & (pos < i32(lens)[:, None])
+    total = torch.where(seen.any(1), heads * group, 0).double()
+    assert ((w.double().sum(1) - total).abs() <= total * 1e-5).all()
+    assert not w[~seen].any() and (w >= 0).all()
+    assert dk.dcp_topk_device_status() == 0

@@ -91,7 +91,9 @@ dcp_status dcp_kv4_read(const dcp_kv4_cache* cache, void* k, void* v, int dtype,
  * A row that sees nothing gives out = 0 and lse = -inf.  Products are exact
  * (fp16 operands: a query row is scaled by a power of two into fp16's range,
  * the cache's values are exact in fp16) and summed in fp32; the probabilities
- * are rounded to fp16 for the second product only, their sum is kept in fp32.
+ * are rounded to fp16 for the second product only, their sum is kept in fp32
+ * (compensated).  Scores beyond 1e8 in magnitude, where fp32's steps span most
+ * of the exponent's range, may give NaN.
  */
 typedef struct {
     const void* q;          /* [rows][q_heads][dim] of dtype (fp16 or bf16), dim contiguous */
@@ -125,8 +127,8 @@ typedef struct {
     int num_seqs;
     int table_width;        /* pages per sequence */
     int num_ids;
-    int max_len;            /* no row's lens exceeds this (0: table_width * page_size); only the
-                               split of the work and the workspace depend on it */
+    int max_len;            /* positions from here on are not seen, whatever lens says (0: the
+                               table's end); the split of the work and the workspace go by it */
     float scale;            /* 0: dim^-1/2 */
     float softcap;          /* 0: none */
 } dcp_kv4_attention_args;

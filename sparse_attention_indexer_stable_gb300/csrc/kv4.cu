@@ -249,7 +249,8 @@ static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
   // whole teams, for tokens by ids (1024 rows x 2048 ids, 8 heads x 128: 518 us
   // against 539) and at dim 64 (33 rows of 12 heads: 23 us against 25).  With
   // ranges at dim 128 their barriers cost more than the lines saved: 248 us
-  // against 232 for 256 rows of up to 8192 tokens.
+  // against 232 for 256 rows of up to 8192 tokens.  (Pairs measured with a plain
+  // running sum of the probabilities; compensated, the first takes 529 us.)
   if constexpr (D < 256)
     if (p.ids && p.together % Shape::kTeam == 0)
       kernel = attention_shares_kernel<D, NT, true, kByTeam>;
@@ -257,9 +258,10 @@ static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
     if (!p.ids && p.together % Shape::kTeam == 0)
       kernel = attention_shares_kernel<D, NT, false, kByTeam>;
   // Ranges of caches whose runs of 8 tokens are 2 KB of codes or more, 8 heads
-  // or 4 (256 rows as above, with a ring or teams and by runs: 8 heads x 64 159
-  // us and 141, x 128 232 and 210, x 256 427 and 396; 4 heads x 128 128 and 121,
-  // x 256 230 and 220; but 4 heads x 64 84 and 85, 2 heads x 256 139 and 147).
+  // or 4 (256 rows as above, with a ring or teams and by runs: 8 heads x 64 161
+  // us and 146, x 128 233 and 213, x 256 437 and 393; 4 heads x 128 129 and 125,
+  // x 256 236 and 222; but, with a plain running sum, 4 heads x 64 84 and 85, 2
+  // heads x 256 139 and 147).
   if (!p.ids && p.c.page_shift >= 3 && p.c.heads == 8) {
     kernel = attention_shares_kernel<D, NT, false, 8>;
     smem = PageStage<D, 8>::kSmem;
@@ -278,8 +280,9 @@ static cudaError_t launch_attention(const AttentionParams& p, const Plan& plan,
                   dim3((unsigned)plan.shares, (unsigned)(heads / kJoinWarps)), 32 * kJoinWarps, 0,
                   1, stream, p);
   // By unit, as many warps to a query head as the SMs hold at the same time (32
-  // each): two rows of 131072 tokens 75, 68, 66, 64 us with 4, 8, 16, 32 warps,
-  // 16 rows of up to 16384 43, 45, 51, 62.
+  // each): rows of 100003 and 131072 tokens 75, 68, 66, 64 us with 4, 8, 16, 32
+  // warps, 16 rows of up to 16384 43, 45, 51, 62 (measured when the shares
+  // before the join still walked by rings, 6 us longer).
   int warps = kMostJoinWarps;
   while (warps > kLeastJoinWarps && plan.cuts * heads * warps > kPlanSms * 32) warps /= 2;
   return launch(join_shares_kernel<D, NT, true>, dim3((unsigned)plan.cuts, (unsigned)heads),

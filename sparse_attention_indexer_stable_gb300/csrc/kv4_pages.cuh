@@ -5,8 +5,8 @@
 // Copied by the warps themselves, a tile at dim 128 takes L1 about 290 cycles
 // (see kv4_team.cuh), more than the 226 that its arithmetic takes an SM; the
 // bulk copies go past that: 16 of them, 37 KB, bring the tiles of 8 warps.  256
-// rows of 64 to 8192 tokens, 8 heads x 128: 210 us against 232; the copies alone
-// take 190, the arithmetic alone 187.
+// rows of 64 to 8192 tokens, 8 heads x 128: 213 us against 233; the copies alone
+// take 190, the arithmetic alone took 187 with a plain running sum (210 us in all).
 //
 // What the barriers cost depends on who has to wait: the warp that fills a stage
 // at once when it has read it itself waits for the slowest of the group (253

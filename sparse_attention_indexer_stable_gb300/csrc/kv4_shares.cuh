@@ -9,9 +9,9 @@
 // 131072 tokens of 8 heads with 64-byte rows read 2.2 times their bytes.
 //
 // Measured (8 heads x 128, 8 query heads each): 256 rows of 64 to 8192 tokens
-// 210 us, 5.8 TB/s, 86% of the measured copy rate (see kv4_pages.cuh).  16 rows
-// of 1 to 16384 tokens 38 us, two of 131072 58 us: there 7 go by before the
-// first tile has landed, 3 to 5 between the median CTA's end and the last one's,
+// 213 us, 5.8 TB/s, 85% of the measured copy rate (see kv4_pages.cuh).  16 rows
+// of 1 to 16384 tokens 39 us, two of 100003 and 131072 58 us: there 7 go by before
+// the first tile has landed, 3 to 5 between the median CTA's end and the last one's,
 // 4 to 6 in the join.
 //
 // Measured and not taken: one producer warp that copies a token's rows of all

@@ -1,11 +1,12 @@
 // kv4_slices.cuh -- attention of short rows: a cluster of 1, 2, 4 or 8 CTAs per
 // row and key/value head, each a slice of the row's tiles dealt to its 8 warps,
-// joined through distributed shared memory.  One launch, no workspace.  Bound
-// by latency: a row of 2048 tokens is one tile per warp and slice, 7 us with 8
+// joined through distributed shared memory.  One launch, and no workspace but the
+// scores where weights are wanted.  Bound by latency: a row of 2048 tokens is one tile per warp and slice, 7 us with 8
 // heads x 128 (with slices joined by a second kernel through a workspace 7 us
-// too, but 3 us more on the host).  16 rows x 2048 ids take 17.7 us in teams of
-// two heads (kv4_team.cuh) and 24.3 with a ring per warp: then L1 takes in lines
-// for 16 us.
+// too, but 3 us more on the host).  16 rows x 2048 ids take 18 us in teams of
+// two heads (kv4_team.cuh) and 24 with a ring per warp: then an SM's L1 takes in
+// lines for 16000 cycles (16 warps, 4 tiles of 128 lines, 2 cycles a line), 8 us,
+// and in teams for half of that.
 #pragma once
 
 #include "kv4_team.cuh"

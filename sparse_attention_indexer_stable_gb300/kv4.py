@@ -185,8 +185,8 @@ def kv4_attention(cache, q, table, lens, ids=None, owner=None, starts=None, row_
     softcap * tanh(score / softcap); 0: none.
     weights: float32 (T, positions), unit column stride: each position's
     probability, summed over the query heads, is added (not with owner).
-    max_len: a host-side bound of lens (0: the table's width); it only shapes
-    the launch, and lens beyond it are cut there.
+    max_len: a host-side bound of lens (0: the table's width); the launch is
+    shaped by it, and positions from it on are not seen.
     A row that sees nothing gives zeros and lse -inf.
     """
     _cache(cache)
@@ -207,7 +207,8 @@ def kv4_evict(cache, table, lens, weights, out_table, budget, sinks=0, recent=0,
     them; out_table: int32 (sequences, at least ceil(budget / page_size)), pages
     that are in no row of table.  A sequence of at most budget tokens keeps
     them all; a longer one keeps its first `sinks`, its last `recent` and the
-    heaviest of the others (equal weights: the lowest position), in order.
+    heaviest of the others (equal weights: the lowest position), in order; a
+    kept token on a hole of table becomes zeros.
     Returns (kept int32 (sequences, budget): the kept positions, ascending, then
     -1; out_lens int32; out_weights float32 (sequences, budget)).
     """

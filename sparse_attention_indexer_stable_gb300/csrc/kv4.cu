@@ -378,7 +378,8 @@ dcp_status dcp_kv4_attention(const dcp_kv4_cache* cache, const dcp_kv4_attention
   dcp_status st = planes_of(cache, &p.c);
   if (st == DCP_OK) st = plan_of(cache, p.c, a, &plan);
   if (st != DCP_OK || a->rows == 0) return st;
-  if (!a->q || !a->lens || !a->out || !a->lse || (!a->table && plan.limit > 0) ||
+  if (!a->q || !a->lens || !a->out || !a->lse ||
+      (!a->table && plan.limit > 0 && a->num_seqs > 0) ||
       (a->owner == nullptr && a->num_seqs < a->rows))
     return DCP_ERR_INVALID;
   if (!aligned(a->out, 16) || !aligned(a->workspace, 16)) return DCP_ERR_INVALID;

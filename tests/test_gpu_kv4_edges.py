@@ -68,3 +68,15 @@ def test_eviction_leaves_nothing_old_where_a_hole_was_kept(dk):  # noqa: F811
         assert (plane[6] == 17 + i).all()
         assert (plane[7, 0] == 17 + i).all() and not plane[7, 1:].any()
         assert not plane[5].any() and (plane[:5] == 17 + i).all()
+
+
+@pytest.mark.parametrize("with_ids", [False, True])
+@pytest.mark.parametrize("heads,width", [(1, 5), (8, 5), (8, 3000)])
+def test_rows_of_a_table_without_sequences_see_nothing(dk, heads, width, with_ids):  # noqa: F811
+    """Every owner is outside an empty table, which has no address."""
+    cache = dk.Kv4Cache.allocate(2, 16, heads, 64, DEV)
+    table = torch.zeros(0, width, dtype=torch.int32, device=DEV)
+    q = torch.ones(3, 2 * heads, 64, dtype=torch.bfloat16, device=DEV)
+    ids = i32([list(range(40))] * 3) if with_ids else None
+    out, lse = dk.kv4_attention(cache, q, table, i32([5, 40, 0]), owner=i32([0, -1, 7]), ids=ids)
+    assert not out.any() and torch.isneginf(lse).all()

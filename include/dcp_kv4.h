@@ -1,8 +1,8 @@
 /*
  * dcp_kv4.h -- C ABI of the 4-bit key/value cache that the selected token ids
- * are read from: writing and reading tokens, attention over a visible range
- * or over the ids of the top-K (dcp_topk.h), and eviction by accumulated
- * attention weight.  GB300 (sm_103a).
+ * are read from: pages and slots for new tokens, writing and reading tokens,
+ * attention over a visible range or over the ids of the top-K (dcp_topk.h), and
+ * eviction by accumulated attention weight.  GB300 (sm_103a).
  *
  * Format.  A token's K (or V) of one head is D elements in blocks of 16.  A
  * block's scale is s = e4m3(min(amax / (6 * unit), 448)) and its codes are
@@ -196,6 +196,57 @@ typedef struct {
  */
 dcp_status dcp_kv4_evict(const dcp_kv4_cache* cache, const dcp_kv4_evict_args* args,
                          dcp_stream_t stream);
+
+/*
+ * dcp_kv4_extend -- pages and slots for the new tokens of a batch.
+ *
+ * Sequence b holds lens[b] tokens and gets counts[b] more (negative values
+ * count as 0).  The new tokens of all sequences take `places` places, one
+ * sequence after the other; tokens behind the last place are not taken in.
+ * Where a sequence's tokens reach beyond the pages that its lens[b] tokens
+ * fill, it takes further pages from the list of free ones, sequence by
+ * sequence, from entry used[0] on, and they are written into its row of the
+ * table.  Pages wanted beyond the list's end are holes (-1); pages beyond the
+ * table's width are not taken.
+ *
+ * Of a place's token: its slot (-1 where its page is a hole or beyond the
+ * table), position, sequence (owner) and the number of positions that it sees
+ * with itself (row_lens).  Places behind the last token: slot -1, position 0,
+ * owner -1, row_lens 0, which dcp_kv4_append skips and dcp_kv4_attention
+ * answers with zeros.  starts[b] is the first place of sequence b, as
+ * dcp_prompt_attention takes it.
+ */
+typedef struct {
+    int32_t* table;             /* [num_seqs][table_width]; the new pages are written */
+    int64_t table_stride;       /* elements between sequences */
+    const int32_t* lens;        /* [num_seqs] */
+    const int32_t* counts;      /* [num_seqs] */
+    const int32_t* free_pages;  /* [num_free], distinct */
+    const int32_t* used;        /* [1]: entries of free_pages given away so far; negative
+                                   counts as 0 */
+    int64_t* slots;             /* [places] */
+    int32_t* positions;         /* [places] */
+    int32_t* owner;             /* [places] */
+    int32_t* row_lens;          /* [places] */
+    int32_t* starts;            /* [num_seqs + 1] */
+    int32_t* out_lens;          /* [num_seqs]: lens with the new tokens; may be lens */
+    int32_t* out_used;          /* [1]: used with the pages wanted, beyond num_free by as many as
+                                   were missing; may be used */
+    int64_t num_pages;          /* of the cache; num_pages * page_size < 2^32 */
+    int page_size;              /* a power of two, at most 65536 */
+    int num_seqs;               /* at most 16384 */
+    int table_width;            /* pages per sequence */
+    int num_free;
+    int places;
+} dcp_kv4_extend_args;
+
+/*
+ * Errors: DCP_ERR_INVALID for negative sizes or a NULL pointer that is needed;
+ * DCP_ERR_UNSUPPORTED for a page size or num_pages outside the limits, more
+ * than 16384 sequences, or more than 2^31 - 1 positions; DCP_ERR_CUDA if the
+ * launch fails.  Positions and lengths stop at 2^31 - 1.
+ */
+dcp_status dcp_kv4_extend(const dcp_kv4_extend_args* args, dcp_stream_t stream);
 
 #ifdef __cplusplus
 }

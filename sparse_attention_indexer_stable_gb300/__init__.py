@@ -1,15 +1,16 @@
 """GB300-native DCP sparse-indexer top-K: a thin Python binding of the C ABI.
 
 The compute lives in ``_build/libdcp_topk.so`` (CUDA, sm_103a), declared in
-``include/dcp_topk.h`` and ``include/dcp_kv4.h``.  This module only marshals torch tensors (device
-memory) and the current CUDA stream into that ABI; every step of the top-K
+``include/dcp_topk.h``, ``include/dcp_kv4.h`` and ``include/dcp_prompt.h``.  This module only
+marshals torch tensors (device memory) and the current CUDA stream into that ABI; every step of the top-K
 runs in the library's kernels.  There is no CPU fallback: if the library is
 missing or fails to load, every call raises.
 
 Functions with the ABI's names take raw device pointers and sizes, exactly like
 the C functions.  ``merge`` and ``local_topk`` are tensor conveniences on top
 of them that check shapes and dtypes and allocate outputs with torch; the
-``kv4_*`` functions (module ``kv4``) are the same for the 4-bit key/value cache.
+``kv4_*`` functions (module ``kv4``) are the same for the 4-bit key/value cache,
+and those of module ``prompt`` for what its new tokens pass before.
 """
 from __future__ import annotations
 
@@ -95,6 +96,12 @@ def library():
             lib.dcp_kv4_attention.restype = I
             lib.dcp_kv4_evict.argtypes = [P, P, P]
             lib.dcp_kv4_evict.restype = I
+            lib.dcp_kv4_extend.argtypes = [P, P]
+            lib.dcp_kv4_extend.restype = I
+            lib.dcp_rotary.argtypes = [P, P]
+            lib.dcp_rotary.restype = I
+            lib.dcp_prompt_attention.argtypes = [P, P]
+            lib.dcp_prompt_attention.restype = I
             lib.dcp_status_string.argtypes = [I]
             lib.dcp_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -393,4 +400,7 @@ def fused_topk(logits, K, L=None, row_starts=None, out_scores=None, out_ids=None
 from . import kv4 as _kv4  # noqa: E402  (uses the helpers above)
 from .kv4 import *  # noqa: E402,F401,F403
 
-__all__ += _kv4.__all__
+from . import prompt as _prompt  # noqa: E402
+from .prompt import *  # noqa: E402,F401,F403
+
+__all__ += _kv4.__all__ + _prompt.__all__

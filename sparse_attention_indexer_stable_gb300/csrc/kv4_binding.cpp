@@ -1,5 +1,6 @@
-// kv4_binding.cpp -- the torch side of the 4-bit cache's functions: checks the
-// tensors, allocates what is not given, calls the C ABI (include/dcp_kv4.h).
+// kv4_binding.cpp -- the torch side of the 4-bit cache's functions and of those
+// that its new tokens pass before: checks the tensors, allocates what is not
+// given, calls the C ABI (include/dcp_kv4.h, include/dcp_prompt.h).
 //
 // In C++ because the smallest calls are bound by the host: on the GB300's CPU
 // the same checks and allocations took 18 us in Python beside 7 us of GPU time
@@ -20,6 +21,7 @@
 #include <string>
 
 #include "dcp_kv4.h"
+#include "dcp_prompt.h"
 
 namespace {
 
@@ -28,6 +30,9 @@ decltype(&dcp_kv4_read) g_read = nullptr;
 decltype(&dcp_kv4_attention_workspace_size) g_workspace_size = nullptr;
 decltype(&dcp_kv4_attention) g_attention = nullptr;
 decltype(&dcp_kv4_evict) g_evict = nullptr;
+decltype(&dcp_kv4_extend) g_extend = nullptr;
+decltype(&dcp_rotary) g_rotary = nullptr;
+decltype(&dcp_prompt_attention) g_prompt = nullptr;
 
 // A Python exception on its way out: `type` with `text`.
 struct Refused {
@@ -153,6 +158,12 @@ float float_of(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
   return (float)v;
+}
+
+int truth_of(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v;
 }
 
 template <typename T>
@@ -390,11 +401,222 @@ PyObject* evict(PyObject*, PyObject* const* p, Py_ssize_t n) {
   });
 }
 
-// connect(append, read, workspace size, attention, evict): their addresses
+// extend(table, lens, counts, free, used, places, page_size, num_pages, out, stream)
+//   -> (slots, positions, owner, row_lens, starts, lens, used) or status
+PyObject* extend(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  if (!takes(n, 10)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &table = needed(p[0], "table"), &lens = needed(p[1], "lens"),
+                     &counts = needed(p[2], "counts"), &free = needed(p[3], "free"),
+                     &used = needed(p[4], "used");
+    if (!table.is_cuda()) value_error("table must be a CUDA tensor");
+    const int dev = table.get_device();
+    check_rows(table, "table", at::kInt, dev, "(sequences, pages)");
+    const int64_t B = table.size(0);
+    if (B > 1 && table.stride(0) < table.size(1))
+      value_error("the rows of table must not overlap");
+    check(lens, "lens", at::kInt, dev, {B});
+    check(counts, "counts", at::kInt, dev, {B});
+    if (free.dim() != 1) value_error("free must be (pages,)");
+    check(free, "free", at::kInt, dev, free.sizes());
+    check(used, "used", at::kInt, dev, {1});
+    dcp_kv4_extend_args a{};
+    a.places = int_of(p[5]);
+    a.page_size = int_of(p[6]);
+    a.num_pages = PyLong_AsLongLong(p[7]);
+    if (a.num_pages == -1 && PyErr_Occurred()) throw python_error();
+    if (a.places < 0) value_error("places must not be negative");
+    const Place place(dev, p[9]);
+    static const char* const names[7] = {"slots", "positions", "owner", "row_lens",
+                                         "starts", "lens", "used"};
+    const int64_t sizes[7] = {a.places, a.places, a.places, a.places, B + 1, B, 1};
+    if (p[8] != Py_None && (!PyTuple_Check(p[8]) || PyTuple_GET_SIZE(p[8]) != 7))
+      type_error("out must be a Kv4Step");
+    at::Tensor out[7];
+    for (int i = 0; i < 7; ++i) {
+      const c10::ScalarType type = i == 0 ? at::kLong : at::kInt;
+      if (p[8] == Py_None) {
+        out[i] = allocate({sizes[i]}, type, dev);
+      } else {
+        const std::string name = std::string("out's ") + names[i];
+        out[i] = needed(PyTuple_GET_ITEM(p[8], i), name.c_str());
+        check(out[i], name.c_str(), type, dev, {sizes[i]});
+      }
+    }
+    a.table = static_cast<int32_t*>(table.data_ptr());
+    a.table_stride = table.stride(0);
+    a.lens = static_cast<const int32_t*>(lens.data_ptr());
+    a.counts = static_cast<const int32_t*>(counts.data_ptr());
+    a.free_pages = static_cast<const int32_t*>(free.data_ptr());
+    a.used = static_cast<const int32_t*>(used.data_ptr());
+    a.slots = static_cast<int64_t*>(out[0].data_ptr());
+    a.positions = static_cast<int32_t*>(out[1].data_ptr());
+    a.owner = static_cast<int32_t*>(out[2].data_ptr());
+    a.row_lens = static_cast<int32_t*>(out[3].data_ptr());
+    a.starts = static_cast<int32_t*>(out[4].data_ptr());
+    a.out_lens = static_cast<int32_t*>(out[5].data_ptr());
+    a.out_used = static_cast<int32_t*>(out[6].data_ptr());
+    a.num_seqs = to_int(B, "sequences");
+    a.table_width = to_int(table.size(1), "pages");
+    a.num_free = to_int(free.size(0), "free");
+    const dcp_status st = call([&] { return g_extend(&a, place.stream); });
+    if (st != DCP_OK) return PyLong_FromLong(st);
+    PyObject* r = PyTuple_New(7);
+    if (!r) return nullptr;
+    for (int i = 0; i < 7; ++i) {
+      PyObject* o = p[8] == Py_None ? THPVariable_Wrap(out[i]) : PyTuple_GET_ITEM(p[8], i);
+      if (!o) {
+        Py_DECREF(r);
+        return nullptr;
+      }
+      if (p[8] != Py_None) Py_INCREF(o);
+      PyTuple_SET_ITEM(r, i, o);
+    }
+    return r;
+  });
+}
+
+// Whether the elements of a (rows, heads, dim) tensor, unit stride along dim,
+// are all at different addresses.
+bool spread_out(const at::Tensor& t) {
+  const int64_t n[2] = {t.size(0), t.size(1)}, s[2] = {t.stride(0), t.stride(1)};
+  if (n[0] == 0 || n[1] == 0) return true;
+  const int wide = s[0] >= s[1] ? 0 : 1;  // the dimension of the larger stride
+  const int64_t inner = n[1 - wide] > 1 ? (n[1 - wide] - 1) * s[1 - wide] : 0;
+  return (n[1 - wide] == 1 || s[1 - wide] >= t.size(2)) &&
+         (n[wide] == 1 || s[wide] >= inner + t.size(2));
+}
+
+// rotary(turns, turned, interleaved, magnitude, positions, q, k, q_out, k_out, stream)
+//   -> (q_out, k_out or None) or status
+PyObject* rotary(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  if (!takes(n, 10)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &turns = needed(p[0], "turns"), &positions = needed(p[4], "positions"),
+                     &q = needed(p[5], "q");
+    const at::Tensor* in[2] = {&q, tensor(p[6], "k")};
+    const at::Tensor* given[2] = {tensor(p[7], "q_out"), tensor(p[8], "k_out")};
+    static const char* const names[2] = {"q", "k"};
+    static const char* const out_names[2] = {"q_out", "k_out"};
+    const int dev = turns.get_device();
+    dcp_rotary_args a{};
+    a.turned = int_of(p[1]);
+    a.interleaved = truth_of(p[2]);
+    a.magnitude = float_of(p[3]);
+    a.dtype = value_type(q, "q", true);
+    if (q.dim() != 3 || q.size(2) < a.turned)
+      value_error("q must be (N, heads, D), D at least the rope's dim = " +
+                  std::to_string(a.turned));
+    a.tokens = q.size(0);
+    a.dim = to_int(q.size(2), "D");
+    check(positions, "positions", at::kInt, dev, {a.tokens});
+    if (given[1] && !in[1]) value_error("k_out needs k");
+    const Place place(dev, p[9]);
+    at::Tensor out[2];
+    for (int i = 0; i < 2; ++i) {
+      if (!in[i]) continue;
+      if (i == 1 && value_type(*in[1], "k", true) != a.dtype)
+        value_error("q and k must be of one dtype");
+      check_values(*in[i], names[i], dev, a.dim);
+      if (in[i]->size(0) != a.tokens) value_error("q and k must have the same tokens");
+      if (given[i]) {
+        check_type(*given[i], out_names[i], q.scalar_type());
+        check_values(*given[i], out_names[i], dev, a.dim);
+        if (given[i]->sizes() != in[i]->sizes())
+          value_error(std::string(out_names[i]) + " must have the shape of " + names[i]);
+        if (!spread_out(*given[i]))
+          value_error("the heads of " + std::string(out_names[i]) + " must not overlap");
+        if (given[i]->data_ptr() == in[i]->data_ptr() && given[i]->strides() != in[i]->strides())
+          value_error(std::string(out_names[i]) + " over " + names[i] + " must have its strides");
+        out[i] = *given[i];
+      } else {
+        out[i] = allocate(in[i]->sizes(), q.scalar_type(), dev);
+      }
+    }
+    a.q = q.data_ptr();
+    a.q_row_stride = q.stride(0), a.q_head_stride = q.stride(1);
+    a.q_out = out[0].data_ptr();
+    a.q_out_row_stride = out[0].stride(0), a.q_out_head_stride = out[0].stride(1);
+    a.q_heads = to_int(q.size(1), "q's heads");
+    if (in[1]) {
+      a.k = in[1]->data_ptr();
+      a.k_row_stride = in[1]->stride(0), a.k_head_stride = in[1]->stride(1);
+      a.k_out = out[1].data_ptr();
+      a.k_out_row_stride = out[1].stride(0), a.k_out_head_stride = out[1].stride(1);
+      a.k_heads = to_int(in[1]->size(1), "k's heads");
+    }
+    a.positions = static_cast<const int32_t*>(positions.data_ptr());
+    a.turns = static_cast<const uint64_t*>(turns.data_ptr());
+    const dcp_status st = call([&] { return g_rotary(&a, place.stream); });
+    if (st != DCP_OK) return PyLong_FromLong(st);
+    if (!in[1]) return Py_BuildValue("(NO)", THPVariable_Wrap(out[0]), Py_None);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out[0]), THPVariable_Wrap(out[1]));
+  });
+}
+
+// prompt_attention(q, k, v, starts, causal, window, scale, softcap, out, lse, stream)
+//   -> (out, lse) or status
+PyObject* prompt_attention(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  if (!takes(n, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &q = needed(p[0], "q"), &k = needed(p[1], "k"), &v = needed(p[2], "v"),
+                     &starts = needed(p[3], "starts");
+    const at::Tensor *given_out = tensor(p[8], "out"), *given_lse = tensor(p[9], "lse");
+    dcp_prompt_attention_args a{};
+    a.dtype = value_type(q, "q", false);
+    if (value_type(k, "k", false) != a.dtype || value_type(v, "v", false) != a.dtype)
+      value_error("q, k and v must be of one dtype");
+    if (!q.is_cuda()) value_error("q must be a CUDA tensor");
+    const int dev = q.get_device();
+    if (q.dim() != 3 || (q.size(2) != 64 && q.size(2) != 128 && q.size(2) != 256))
+      value_error("q must be (T, heads, D), D 64, 128 or 256");
+    a.dim = (int)q.size(2);
+    check_values(q, "q", dev, a.dim);
+    check_values(k, "k", dev, a.dim);
+    check_values(v, "v", dev, a.dim);
+    a.rows = q.size(0);
+    if (k.size(0) != a.rows || v.sizes() != k.sizes())
+      value_error("k and v must both be (T, heads, D) with q's T");
+    if (k.size(1) < 1 || q.size(1) < 1 || q.size(1) % k.size(1))
+      value_error("q's heads must be a multiple of k's");
+    a.q_heads = to_int(q.size(1), "q's heads");
+    a.kv_heads = to_int(k.size(1), "k's heads");
+    if (starts.dim() != 1 || starts.size(0) < 1) value_error("starts must be (sequences + 1,)");
+    check(starts, "starts", at::kInt, dev, starts.sizes());
+    a.num_seqs = to_int(starts.size(0) - 1, "sequences");
+    a.causal = truth_of(p[4]);
+    a.window = int_of(p[5]);
+    if (a.window < 0) value_error("window must not be negative");
+    a.scale = p[6] == Py_None ? 0.0f : float_of(p[6]);
+    if (!std::isfinite(a.scale)) value_error("scale must be finite");
+    a.softcap = float_of(p[7]);
+    if (!std::isfinite(a.softcap) || a.softcap < 0.0f)
+      value_error("softcap must be finite and not negative");
+    const int64_t out_shape[3] = {a.rows, a.q_heads, a.dim}, lse_shape[2] = {a.rows, a.q_heads};
+    const Place place(dev, p[10]);
+    if (given_out) check(*given_out, "out", q.scalar_type(), dev, out_shape);
+    if (given_lse) check(*given_lse, "lse", at::kFloat, dev, lse_shape);
+    const at::Tensor out = given_out ? *given_out : allocate(out_shape, q.scalar_type(), dev);
+    const at::Tensor lse = given_lse ? *given_lse : allocate(lse_shape, at::kFloat, dev);
+    a.q = q.data_ptr(), a.k = k.data_ptr(), a.v = v.data_ptr();
+    a.q_row_stride = q.stride(0), a.q_head_stride = q.stride(1);
+    a.k_row_stride = k.stride(0), a.k_head_stride = k.stride(1);
+    a.v_row_stride = v.stride(0), a.v_head_stride = v.stride(1);
+    a.starts = static_cast<const int32_t*>(starts.data_ptr());
+    a.out = out.data_ptr();
+    a.lse = static_cast<float*>(lse.data_ptr());
+    const dcp_status st = call([&] { return g_prompt(&a, place.stream); });
+    if (st != DCP_OK) return PyLong_FromLong(st);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
+  });
+}
+
+// connect(append, read, workspace size, attention, evict, extend, rotary, prompt
+// attention): their addresses
 PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!takes(n, 5)) return nullptr;
-  void* f[5];
-  for (int i = 0; i < 5; ++i) {
+  if (!takes(n, 8)) return nullptr;
+  void* f[8];
+  for (int i = 0; i < 8; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null entry point");
@@ -406,6 +628,9 @@ PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_workspace_size = reinterpret_cast<decltype(g_workspace_size)>(f[2]);
   g_attention = reinterpret_cast<decltype(g_attention)>(f[3]);
   g_evict = reinterpret_cast<decltype(g_evict)>(f[4]);
+  g_extend = reinterpret_cast<decltype(g_extend)>(f[5]);
+  g_rotary = reinterpret_cast<decltype(g_rotary)>(f[6]);
+  g_prompt = reinterpret_cast<decltype(g_prompt)>(f[7]);
   Py_RETURN_NONE;
 }
 
@@ -419,6 +644,9 @@ PyMethodDef g_methods[] = {
     {"read", fast(read), METH_FASTCALL, nullptr},
     {"attention", fast(attention), METH_FASTCALL, nullptr},
     {"evict", fast(evict), METH_FASTCALL, nullptr},
+    {"extend", fast(extend), METH_FASTCALL, nullptr},
+    {"rotary", fast(rotary), METH_FASTCALL, nullptr},
+    {"prompt_attention", fast(prompt_attention), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1,0 +1,168 @@
+// kv4_extend.cuh -- pages and slots for the new tokens of a batch.
+//
+// With n_b new tokens of sequence b that holds l_b, two exclusive sums decide
+// everything: starts_b = sum n (cut at the places), first_b = used + sum of
+// pages(l + n) - pages(l).  The token at place t of sequence b is at position
+// p = l_b + t - starts_b, in page table[p / P] if that was there before and in
+// free[first_b + p / P - pages(l_b)] otherwise; the token that opens a page
+// also writes it into the table.
+//
+// One cluster of up to 8 CTAs in one launch: each CTA sums over all sequences
+// (a few numbers per thread), so that nothing has to be passed between CTAs,
+// and takes its stripe of the places.  The cluster's barrier stands between the
+// last read of lens and used and their new values, which may go to the same
+// memory.
+#pragma once
+
+#include "kv4_common.cuh"
+
+namespace dcp {
+namespace kv4 {
+
+constexpr int kExtendThreads = 1024;
+constexpr int kMostExtendSeqs = 16384;
+constexpr int kExtendRow = 12;  // bytes of shared memory for a sequence
+
+struct ExtendParams {
+  int32_t* table;
+  int64_t table_stride;
+  const int32_t *lens, *counts, *free_pages, *used;
+  int64_t* slots;
+  int32_t *positions, *owner, *row_lens, *starts, *out_lens, *out_used;
+  uint32_t num_pages;
+  int page_shift, num_seqs, table_width, num_free, places;
+};
+
+__device__ __forceinline__ int clamp_int(int64_t x) {
+  return x > INT32_MAX ? INT32_MAX : (int)x;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Inclusive sum over the CTA's threads; `total` gets the sum of all.
+__device__ __forceinline__ int64_t cta_sum(int64_t x, int64_t* warp_sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int64_t w = warp_sums[lane];  // as many warps as lanes
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t y = __shfl_up_sync(~0u, w, d);
+    if (lane >= d) w += y;
+  }
+  *total = __shfl_sync(~0u, w, 31);
+  const int64_t before = __shfl_sync(~0u, w, warp ? warp - 1 : 0);
+  __syncthreads();  // warp_sums may be used again
+  return x + (warp ? before : 0);
+}
+
+__global__ void __launch_bounds__(kExtendThreads, 1) extend_kernel(const ExtendParams p) {
+  extern __shared__ int32_t extend_smem[];
+  static_assert(kExtendThreads == 32 * 32, "cta_sum takes as many warps as lanes");
+  __shared__ int64_t warp_sums[32];
+  int32_t* s_start = extend_smem;              // first place
+  int32_t* s_len = s_start + p.num_seqs;       // tokens held
+  int32_t* s_first = s_len + p.num_seqs;       // first new page's entry of free_pages
+  grid_dependency_wait();
+
+  const int64_t size = (int64_t)1 << p.page_shift;
+  auto pages = [&](int64_t tokens) {  // that are in the table
+    const int64_t n = (tokens + size - 1) >> p.page_shift;
+    return n < p.table_width ? n : (int64_t)p.table_width;
+  };
+  const int32_t used = max(*p.used, 0);
+  int64_t tokens = 0, taken = used;  // in the sequences before `base`
+  for (int base = 0; base < p.num_seqs; base += kExtendThreads) {
+    const int b = base + threadIdx.x;
+    int64_t count = 0, len = 0, sum;
+    if (b < p.num_seqs) count = max(p.counts[b], 0), len = max(p.lens[b], 0);
+    const int64_t end = tokens + cta_sum(count, warp_sums, &sum);
+    tokens += sum;
+    const int64_t first_place = min(end - count, (int64_t)p.places);
+    const int64_t fresh = min(end, (int64_t)p.places) - first_place;
+    const int64_t wanted = pages(len + fresh) - pages(len);
+    const int64_t last = taken + cta_sum(wanted, warp_sums, &sum);
+    taken += sum;
+    if (b < p.num_seqs) {
+      s_start[b] = (int)first_place;
+      s_len[b] = (int)len;
+      s_first[b] = clamp_int(last - wanted);
+    }
+  }
+  const int total = (int)min(tokens, (int64_t)p.places);
+  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  cluster_arrive();  // this CTA has read its lens and used
+  __syncthreads();
+
+  for (int64_t t = (int64_t)rank * kExtendThreads + threadIdx.x; t < p.places;
+       t += (int64_t)ctas * kExtendThreads) {
+    int64_t slot = -1;
+    int position = 0, owner = -1, sees = 0;
+    if (t < total) {
+      // the last sequence that starts at or before t: of several that start at
+      // the same place only the last has a token
+      int lo = 0, hi = p.num_seqs;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= t) lo = mid; else hi = mid;
+      }
+      const int64_t len = s_len[lo], at = len + t - s_start[lo];
+      const int64_t had = pages(len), index = at >> p.page_shift;
+      owner = lo;
+      position = clamp_int(at);
+      sees = clamp_int(at + 1);
+      if (index < p.table_width) {
+        int32_t* entry = p.table + lo * p.table_stride + index;
+        int32_t page = -1;
+        if (index < had) {
+          page = *entry;
+        } else {
+          const int64_t from = s_first[lo] + (index - had);
+          if (from < p.num_free) page = p.free_pages[from];
+          if ((at & (size - 1)) == 0) *entry = page;  // the page's first token
+        }
+        if ((uint32_t)page < p.num_pages) slot = ((int64_t)page << p.page_shift) + (at & (size - 1));
+      }
+    }
+    p.slots[t] = slot;
+    p.positions[t] = position;
+    p.owner[t] = owner;
+    p.row_lens[t] = sees;
+  }
+
+  __syncwarp();
+  cluster_wait();  // every CTA has read lens and used
+  for (int b = rank * kExtendThreads + threadIdx.x; b <= p.num_seqs; b += ctas * kExtendThreads) {
+    const int first_place = b < p.num_seqs ? s_start[b] : total;
+    p.starts[b] = first_place;
+    if (b == p.num_seqs) {
+      *p.out_used = clamp_int(taken);
+      continue;
+    }
+    const int next = b + 1 < p.num_seqs ? s_start[b + 1] : total;
+    p.out_lens[b] = clamp_int((int64_t)s_len[b] + (next - first_place));
+  }
+}
+
+}  // namespace kv4
+}  // namespace dcp

@@ -2,7 +2,7 @@
 ABI of include/dcp_kv4.h.
 
 ``Kv4Cache`` is a handle on four torch tensors (codes and scales of K and V in
-pages); ``kv4_append`` and ``kv4_read`` write tokens and read them back,
+pages); ``kv4_extend`` gives a batch's new tokens pages and slots, ``kv4_append`` and ``kv4_read`` write tokens and read them back,
 ``kv4_attention`` attends over every visible position of a row or over the ids
 that ``merge`` and ``fused_topk`` give, ``kv4_evict`` keeps a sequence's
 heaviest tokens.  As in the rest of the package all the work runs in the
@@ -16,10 +16,11 @@ import functools
 import importlib.util
 import struct
 import threading
+from typing import Any, NamedTuple
 
 from . import DCP_OK, DcpError, _build, _check, _torch, library
 
-__all__ = ["Kv4Cache", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_workspace_size",
+__all__ = ["Kv4Cache", "Kv4Step", "kv4_extend", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_workspace_size",
            "kv4_evict", "DCP_F16", "DCP_BF16", "DCP_F32"]
 
 DCP_F16, DCP_BF16, DCP_F32 = 0, 1, 2
@@ -46,7 +47,8 @@ def _bind():
             spec.loader.exec_module(module)
             module.connect(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.dcp_kv4_append, lib.dcp_kv4_read, lib.dcp_kv4_attention_workspace_size,
-                lib.dcp_kv4_attention, lib.dcp_kv4_evict)])
+                lib.dcp_kv4_attention, lib.dcp_kv4_evict, lib.dcp_kv4_extend, lib.dcp_rotary,
+                lib.dcp_prompt_attention)])
             _bound = module
     return _bound
 
@@ -121,6 +123,43 @@ class Kv4Cache:
 def _cache(cache):
     if not isinstance(cache, Kv4Cache):
         raise TypeError("cache must be a Kv4Cache")
+
+
+class Kv4Step(NamedTuple):
+    """What kv4_extend says of a batch's places and sequences."""
+
+    slots: Any       # int64 (places,): page * page_size + offset, -1 for none
+    positions: Any   # int32 (places,)
+    owner: Any       # int32 (places,): the sequence, -1 behind the last token
+    row_lens: Any    # int32 (places,): the positions that a token sees with itself
+    starts: Any      # int32 (sequences + 1,): a sequence's first place
+    lens: Any        # int32 (sequences,): tokens held, the new ones included
+    used: Any        # int32 (1,): entries of the free list given away
+
+
+def kv4_extend(table, lens, counts, free, used, places, page_size, num_pages, out=None,
+               stream=None):
+    """Pages and slots for a batch's new tokens: a Kv4Step.
+
+    Sequence b holds lens[b] tokens and gets counts[b] more (int32 (sequences,)
+    both); the new tokens lie one sequence after the other in `places` places,
+    the rest of which is padding (slot -1, position 0, owner -1, row_lens 0:
+    kv4_append skips it, kv4_attention answers it with zeros).  Tokens beyond
+    the places are not taken in.
+    table: int32 (sequences, pages per sequence), written where a sequence
+    reaches a new page: the next ones of free (int32, distinct pages), from
+    entry used[0] on (int32 (1,)).  Where the list ends, the table gets holes
+    (-1), their tokens no slot, and the new `used` passes len(free) by the pages
+    that were missing.
+    page_size and num_pages are those of the caches that the table serves.
+    out: an earlier Kv4Step to write to; its lens may be `lens` and its used
+    `used`, which then advance in place.
+    """
+    r = (_bound or _bind()).extend(table, lens, counts, free, used, places, page_size, num_pages,
+                                   out, _handle(stream))
+    if type(r) is int:
+        _raise(r, "dcp_kv4_extend")
+    return Kv4Step._make(r)
 
 
 def kv4_append(cache, k, v, slots, stream=None):

@@ -111,9 +111,14 @@ typedef struct {
  * Errors: DCP_ERR_INVALID for a bad dtype, negative sizes or window, a softcap
  * that is negative, a softcap or scale that is not finite, q_heads not a
  * multiple of kv_heads, or a NULL pointer with rows and num_seqs > 0;
- * DCP_ERR_UNSUPPORTED for a dim outside the limits or sizes whose products pass
- * 2^31 - 1 (rows * q_heads); DCP_ERR_CUDA if a launch fails.
- * rows == 0 and num_seqs == 0 are no-ops.
+ * DCP_ERR_UNSUPPORTED for a dim outside the limits, sizes whose products pass
+ * 2^31 - 1 (rows * q_heads), more than 65536 heads, or a q, k or v that tensor
+ * copies cannot read: it is not 16-byte aligned, or a stride (of a dimension of
+ * more than one element) is not a positive multiple of 8 elements;
+ * DCP_ERR_CUDA if a launch fails.  rows == 0 and num_seqs == 0 are no-ops.
+ * Waits are bounded: a CTA one of whose copies does not land within about a
+ * second gives up.  Then DCP_DEVICE_COPY_TIMEOUT is set in the device status
+ * word (dcp_topk_device_status), and the rows that it had not finished are NaN.
  */
 dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* args, dcp_stream_t stream);
 

@@ -554,6 +554,18 @@ PyObject* rotary(PyObject*, PyObject* const* p, Py_ssize_t n) {
   });
 }
 
+// t where tensor copies can read it (16-byte steps between its rows and heads,
+// none of 0); otherwise a copy that they can.
+at::Tensor for_tensor_copies(const at::Tensor& t) {
+  bool fits = ((uintptr_t)t.data_ptr() & 15) == 0;
+  for (int i = 0; i < 2; ++i)
+    fits = fits && (t.size(i) <= 1 || (t.stride(i) > 0 && t.stride(i) % 8 == 0));
+  if (fits) return t;
+  at::Tensor copy = allocate(t.sizes(), t.scalar_type(), t.get_device());
+  copy.copy_(t, true);
+  return copy;
+}
+
 // prompt_attention(q, k, v, starts, causal, window, scale, softcap, out, lse, stream)
 //   -> (out, lse) or status
 PyObject* prompt_attention(PyObject*, PyObject* const* p, Py_ssize_t n) {
@@ -598,10 +610,12 @@ PyObject* prompt_attention(PyObject*, PyObject* const* p, Py_ssize_t n) {
     if (given_lse) check(*given_lse, "lse", at::kFloat, dev, lse_shape);
     const at::Tensor out = given_out ? *given_out : allocate(out_shape, q.scalar_type(), dev);
     const at::Tensor lse = given_lse ? *given_lse : allocate(lse_shape, at::kFloat, dev);
-    a.q = q.data_ptr(), a.k = k.data_ptr(), a.v = v.data_ptr();
-    a.q_row_stride = q.stride(0), a.q_head_stride = q.stride(1);
-    a.k_row_stride = k.stride(0), a.k_head_stride = k.stride(1);
-    a.v_row_stride = v.stride(0), a.v_head_stride = v.stride(1);
+    const at::Tensor qc = for_tensor_copies(q), kc = for_tensor_copies(k),
+                     vc = for_tensor_copies(v);
+    a.q = qc.data_ptr(), a.k = kc.data_ptr(), a.v = vc.data_ptr();
+    a.q_row_stride = qc.stride(0), a.q_head_stride = qc.stride(1);
+    a.k_row_stride = kc.stride(0), a.k_head_stride = kc.stride(1);
+    a.v_row_stride = vc.stride(0), a.v_head_stride = vc.stride(1);
     a.starts = static_cast<const int32_t*>(starts.data_ptr());
     a.out = out.data_ptr();
     a.lse = static_cast<float*>(lse.data_ptr());

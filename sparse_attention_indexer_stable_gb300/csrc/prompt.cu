@@ -1,17 +1,129 @@
 // prompt.cu -- C ABI of attention over whole prompts (include/dcp_prompt.h).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <climits>
 #include <cmath>
 #include <cstdint>
 
+#include <atomic>
+#include <mutex>
+
 #include "dcp_prompt.h"
-#include "prompt_rows.cuh"
+#include "prompt_tiles.cuh"
 
 using namespace dcp;
 using namespace dcp::prompt;
 
 static dcp_status status_of(cudaError_t e) { return e == cudaSuccess ? DCP_OK : DCP_ERR_CUDA; }
+
+// ------------------------------------------------------------------ devices
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static std::atomic<bool> g_ready[64];
+static unsigned int* g_status[64];  // each device's status word, before g_ready
+static EncodeTiled g_encode;        // likewise
+static std::mutex g_mutex;
+
+template <int D, bool kHalf>
+static cudaError_t allow_tiles() {
+  constexpr int kBytes = sizeof(Shared<D>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D, kHalf, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(tiles_kernel<D, kHalf, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  return e;
+}
+
+// Per-device kernel attributes, set once (the first call on a device must
+// therefore not be inside a stream capture).
+static cudaError_t prepare_device(unsigned int** status) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!g_ready[dev].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if ((e = allow_tiles<64, false>()) != cudaSuccess ||
+        (e = allow_tiles<64, true>()) != cudaSuccess ||
+        (e = allow_tiles<128, false>()) != cudaSuccess ||
+        (e = allow_tiles<128, true>()) != cudaSuccess ||
+        (e = allow_tiles<256, false>()) != cudaSuccess ||
+        (e = allow_tiles<256, true>()) != cudaSuccess ||
+        (e = device_status_word(&g_status[dev])) != cudaSuccess)
+      return e;
+    if (!g_encode) {
+      void* f = nullptr;
+      cudaDriverEntryPointQueryResult found;
+      e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                           &found);
+      if (e != cudaSuccess) return e;
+      if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+      g_encode = reinterpret_cast<EncodeTiled>(f);
+    }
+    g_ready[dev].store(true, std::memory_order_release);
+  }
+  *status = g_status[dev];
+  return cudaSuccess;
+}
+
+// ------------------------------------------------------------- tensor copies
+// Whether tensor copies can read heads laid out so: 16-byte steps, none of 0.
+static bool fits(const void* x, int64_t rows, int64_t row_stride, int heads, int64_t head_stride) {
+  const int64_t most = (int64_t)1 << 38;  // elements: 2^39 bytes
+  return ((uintptr_t)x & 15) == 0 &&
+         (rows == 1 || (row_stride > 0 && row_stride < most && row_stride % 8 == 0)) &&
+         (heads == 1 || (head_stride > 0 && head_stride < most && head_stride % 8 == 0));
+}
+
+// Boxes of `tokens` rows of `packed` heads, 64 elements each.
+static bool map_of(CUtensorMap* map, const void* x, int dtype, int64_t rows, int64_t row_stride,
+                   int heads, int64_t head_stride, int dim, int packed, int tokens) {
+  const cuuint64_t sizes[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  // a dimension of one element may have any stride
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads == 1 ? dim : head_stride) * 2,
+                                 (cuuint64_t)(rows == 1 ? dim : row_stride) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)packed, (cuuint32_t)tokens};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return g_encode(map, dtype == DCP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  3, const_cast<void*>(x), sizes, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+static dcp_status launch_tiles(const dcp_prompt_attention_args* a, TileParams p,
+                               cudaStream_t stream) {
+  using S = Shape<D>;
+  const int group = p.p.group;
+  p.packed = group < kTileRows ? group : kTileRows;
+  while (group % p.packed) --p.packed;
+  p.tokens = kTileRows / p.packed;
+  p.sets = a->q_heads / p.packed;
+  p.q_bytes = S::kChunks * p.packed * p.tokens * 128;
+  CUtensorMap q, k, v;
+  if (!map_of(&q, a->q, a->dtype, a->rows, a->q_row_stride, a->q_heads, a->q_head_stride, D,
+              p.packed, p.tokens) ||
+      !map_of(&k, a->k, a->dtype, a->rows, a->k_row_stride, a->kv_heads, a->k_head_stride, D, 1,
+              S::kKeys) ||
+      !map_of(&v, a->v, a->dtype, a->rows, a->v_row_stride, a->kv_heads, a->v_head_stride, D, 1,
+              S::kKeys))
+    return DCP_ERR_CUDA;
+  // as many units as there can be, whatever the lengths
+  const int64_t by_span = a->rows / (S::kTiles * p.tokens) + a->num_seqs;
+  const int64_t units = by_span < a->rows ? by_span : a->rows;
+  const bool half = a->dtype == DCP_F16;
+  auto* kernel = half ? (p.p.capped ? tiles_kernel<D, true, true> : tiles_kernel<D, true, false>)
+                      : (p.p.capped ? tiles_kernel<D, false, true> : tiles_kernel<D, false, false>);
+  return status_of(kv4::launch(kernel, dim3((unsigned)(units * p.sets)), S::kThreads,
+                               sizeof(Shared<D>) + 1024, 1, stream, p, q, k, v));
+}
 
 extern "C" dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* a,
                                            dcp_stream_t stream) {
@@ -25,7 +137,12 @@ extern "C" dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* a,
   if (a->rows == 0 || a->num_seqs == 0) return DCP_OK;
   if (!a->q || !a->k || !a->v || !a->starts || !a->out || !a->lse || ((uintptr_t)a->out & 15))
     return DCP_ERR_INVALID;
-  Params p{};
+  if (!fits(a->q, a->rows, a->q_row_stride, a->q_heads, a->q_head_stride) ||
+      !fits(a->k, a->rows, a->k_row_stride, a->kv_heads, a->k_head_stride) ||
+      !fits(a->v, a->rows, a->v_row_stride, a->kv_heads, a->v_head_stride))
+    return DCP_ERR_UNSUPPORTED;
+  TileParams t{};
+  Params& p = t.p;
   p.q = a->q, p.k = a->k, p.v = a->v;
   p.q_row_stride = a->q_row_stride, p.q_head_stride = a->q_head_stride;
   p.k_row_stride = a->k_row_stride, p.k_head_stride = a->k_head_stride;
@@ -47,7 +164,9 @@ extern "C" dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* a,
   // finite, and above 0: 0 times it stays 0, an infinity one
   p.mult = copysignf(fminf(fmaxf(fabsf(p.capped ? scale / a->softcap : scale * kLog2e), 1e-37f),
                            3e38f), scale);
-  const dim3 grid((unsigned)p.rows, (unsigned)((p.q_heads + kRowWarps - 1) / kRowWarps));
-  auto* kernel = a->dim == 64 ? rows_kernel<64> : a->dim == 128 ? rows_kernel<128> : rows_kernel<256>;
-  return status_of(kv4::launch(kernel, grid, 32 * kRowWarps, 0, 1, (cudaStream_t)stream, p));
+  if (prepare_device(&t.status) != cudaSuccess) return DCP_ERR_CUDA;
+  const cudaStream_t st = (cudaStream_t)stream;
+  return a->dim == 64    ? launch_tiles<64>(a, t, st)
+         : a->dim == 128 ? launch_tiles<128>(a, t, st)
+                         : launch_tiles<256>(a, t, st);
 }

@@ -1,5 +1,6 @@
 // prompt_rows.cuh -- attention over whole prompts, one row and head to a warp,
-// on the plain arithmetic units.
+// on the plain arithmetic units: for rows that the tensor cores cannot do (see
+// prompt_tiles.cuh), about a thousandth of their speed.
 //
 // With x_j = s_j / ln 2 and a reference r that is a running maximum,
 //   l = sum 2^(x_j - r),  out = sum 2^(x_j - r) v_j / l,  lse = ln 2 * (r + log2 l);
@@ -108,25 +109,6 @@ __device__ __forceinline__ void attend_row(const Params& p, int first, int n, in
       static_cast<__half*>(p.out)[at] = __float2half_rn(y);
   }
   if (lane == 0) p.lse[out_row] = l == 0.0f ? -INFINITY : kLn2 * (r + log2f(l));
-}
-
-constexpr int kRowWarps = 8;
-
-// A CTA per row and eight heads.
-template <int D>
-__global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const Params p) {
-  __shared__ float q_rows[kRowWarps][D];
-  kv4::grid_dependency_wait();
-  const int t = blockIdx.x, h = blockIdx.y * kRowWarps + threadIdx.x / 32;
-  // the last sequence that starts at or before t
-  int lo = 0, hi = p.num_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start_of(p, mid) <= t) lo = mid; else hi = mid;
-  }
-  const int first = start_of(p, lo), n = start_of(p, lo + 1) - first;
-  if (t < first || t >= first + n || h >= p.q_heads) return;
-  attend_row<D>(p, first, n, t - first, h, q_rows[threadIdx.x / 32]);
 }
 
 }  // namespace prompt

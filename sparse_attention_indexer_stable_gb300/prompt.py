@@ -104,8 +104,9 @@ def prompt_attention(q, k, v, starts, causal=True, window=0, scale=None, softcap
     float32 (T, q_heads), natural logarithm).
 
     q: float16 or bfloat16 (T, q_heads, D), D 64, 128 or 256; k, v: (T, heads, D)
-    of q's dtype; any row and head strides; query head h reads key/value head
-    h // (q_heads // heads).
+    of q's dtype; query head h reads key/value head h // (q_heads // heads).  Any
+    row and head strides; what is not 16-byte aligned, or whose strides are 0 or
+    no multiples of 8 elements, is copied first.
     starts: int32 (sequences + 1,), ascending, as kv4_extend gives them: sequence
     b is rows starts[b] to starts[b + 1] - 1.  Row i of a sequence sees its rows
     j <= i (all of them with causal=False) and, with a window, j > i - window.

@@ -91,6 +91,9 @@ def test_rotary_argument_errors(change, want):
     (dict(out=0), dk.DCP_ERR_INVALID), (dict(lse=0), dk.DCP_ERR_INVALID),
     (dict(out=FAKE + 2), dk.DCP_ERR_INVALID), (dict(dim=96), dk.DCP_ERR_UNSUPPORTED),
     (dict(rows=1 << 30), dk.DCP_ERR_UNSUPPORTED), (dict(rows=1 << 40), dk.DCP_ERR_UNSUPPORTED),
+    (dict(q=FAKE + 2), dk.DCP_ERR_UNSUPPORTED), (dict(k_row=132), dk.DCP_ERR_UNSUPPORTED),
+    (dict(v_row=0), dk.DCP_ERR_UNSUPPORTED), (dict(q_head=-8), dk.DCP_ERR_UNSUPPORTED),
+    (dict(q_row=1 << 39), dk.DCP_ERR_UNSUPPORTED),
     (dict(rows=0, q=0, k=0, out=0), dk.DCP_OK), (dict(num_seqs=0), dk.DCP_OK),
 ])
 def test_prompt_argument_errors(change, want):

@@ -25,6 +25,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 
 static std::atomic<bool> g_ready[64];
 static unsigned int* g_status[64];  // each device's status word, before g_ready
+static int g_sms[64];               // and its SMs
 static EncodeTiled g_encode;        // likewise
 static std::mutex g_mutex;
 
@@ -41,7 +42,7 @@ static cudaError_t allow_tiles() {
 
 // Per-device kernel attributes, set once (the first call on a device must
 // therefore not be inside a stream capture).
-static cudaError_t prepare_device(unsigned int** status) {
+static cudaError_t prepare_device(TileParams* p) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -54,6 +55,8 @@ static cudaError_t prepare_device(unsigned int** status) {
         (e = allow_tiles<128, true>()) != cudaSuccess ||
         (e = allow_tiles<256, false>()) != cudaSuccess ||
         (e = allow_tiles<256, true>()) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev)) !=
+            cudaSuccess ||
         (e = device_status_word(&g_status[dev])) != cudaSuccess)
       return e;
     if (!g_encode) {
@@ -67,7 +70,8 @@ static cudaError_t prepare_device(unsigned int** status) {
     }
     g_ready[dev].store(true, std::memory_order_release);
   }
-  *status = g_status[dev];
+  p->status = g_status[dev];
+  p->sms = g_sms[dev];
   return cudaSuccess;
 }
 
@@ -111,9 +115,9 @@ static dcp_status launch_tiles(const dcp_prompt_attention_args* a, TileParams p,
   if (!map_of(&q, a->q, a->dtype, a->rows, a->q_row_stride, a->q_heads, a->q_head_stride, D,
               p.packed, p.tokens) ||
       !map_of(&k, a->k, a->dtype, a->rows, a->k_row_stride, a->kv_heads, a->k_head_stride, D, 1,
-              S::kKeys) ||
+              kKeys) ||
       !map_of(&v, a->v, a->dtype, a->rows, a->v_row_stride, a->kv_heads, a->v_head_stride, D, 1,
-              S::kKeys))
+              kKeys))
     return DCP_ERR_CUDA;
   // as many units as there can be, whatever the lengths
   const int64_t by_span = a->rows / (S::kTiles * p.tokens) + a->num_seqs;
@@ -164,7 +168,7 @@ extern "C" dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* a,
   // finite, and above 0: 0 times it stays 0, an infinity one
   p.mult = copysignf(fminf(fmaxf(fabsf(p.capped ? scale / a->softcap : scale * kLog2e), 1e-37f),
                            3e38f), scale);
-  if (prepare_device(&t.status) != cudaSuccess) return DCP_ERR_CUDA;
+  if (prepare_device(&t) != cudaSuccess) return DCP_ERR_CUDA;
   const cudaStream_t st = (cudaStream_t)stream;
   return a->dim == 64    ? launch_tiles<64>(a, t, st)
          : a->dim == 128 ? launch_tiles<128>(a, t, st)

@@ -46,20 +46,15 @@ __device__ __forceinline__ float score_of(const Params& p, float dot) {
 }
 
 // Row t (row i of the sequence that starts at row `first` and has n rows), head
-// h, by one warp.  q_row: D floats of shared memory of the warp's own.
+// h, by one warp.
 template <int D>
-__device__ __forceinline__ void attend_row(const Params& p, int first, int n, int i, int h,
-                                           float* q_row) {
+__device__ __forceinline__ void attend_row(const Params& p, int first, int n, int i, int h) {
   const int lane = threadIdx.x & 31;
   const int64_t t = first + i;
   const int kv = h / p.group;
   const int from = p.window ? max(0, i - p.window + 1) : 0, to = p.causal ? i + 1 : n;
-  __syncwarp();
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e)
-    q_row[lane + 32 * e] = kv4::load_element(
-        p.q, t * p.q_row_stride + h * p.q_head_stride + lane + 32 * e, p.dtype);
-  __syncwarp();
+  const int64_t q_at = t * p.q_row_stride + h * p.q_head_stride;
+  __syncwarp();  // after what other lanes have written to this row
   float acc[D / 32], r = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
@@ -71,7 +66,9 @@ __device__ __forceinline__ void attend_row(const Params& p, int first, int n, in
       float dot = 0.0f;
       const int64_t at = key * p.k_row_stride + kv * p.k_head_stride;
 #pragma unroll 16
-      for (int e = 0; e < D; ++e) dot = fmaf(q_row[e], kv4::load_element(p.k, at + e, p.dtype), dot);
+      for (int e = 0; e < D; ++e)
+        dot = fmaf(kv4::load_element(p.q, q_at + e, p.dtype),
+                   kv4::load_element(p.k, at + e, p.dtype), dot);
       x = score_of(p, dot);
     }
     float top = x;

@@ -1,11 +1,11 @@
 // prompt_tiles.cuh -- attention over whole prompts on the tensor cores.
 //
-// A CTA takes one or two tiles of 128 query rows of one key/value head and
-// walks over the keys that they see, a step of keys at a time:
+// A unit of work is one or two tiles of 128 query rows of one key/value head.
+// It walks over the keys that its rows see, 128 a step:
 //
 //   S = Q K^T        tensor cores, operands in shared memory, S in tensor memory
 //   P = 2^(S mult - ref), l += sum P      four warps a tile, a row a thread
-//   O += P V         tensor cores, P in tensor memory over S, O in tensor memory
+//   O += P V         tensor cores, P and O in tensor memory
 //
 // A tile's rows are p query heads that share the key/value head times 128 / p
 // tokens, so that a short prompt still fills the tile and the diagonal cuts off
@@ -14,14 +14,23 @@
 // passed it by 2^15, so that O is rarely read before the end.  P stays below
 // fp16's 65504, and fp16's smallest step, 2^-24, is 2^-32 of the largest P.
 //
-// Two tiles take turns: while one's rows are exponentiated, the tensor cores
-// work on the other's.  One warp issues the products, one the tensor copies
-// (K and V of a step in turn through a ring of stages).
+// What bounds a step is the tensor cores' time for both products, or, for heads
+// of 64, the exponentials; the rest has to happen meanwhile:
+// - Two tiles take turns: while one's rows are exponentiated, the tensor cores
+//   work on the other's.
+// - Heads of 128: S and O of two tiles fill tensor memory, P takes S's place.
+//   Heads of 64 and 256 (one tile) leave room for P beside S, and the next S is
+//   computed as soon as the rows have read the last.
+// - P comes in two halves, and its product begins with the first.
+// - A CTA stays on its SM and takes unit after unit: one warp fetches the next
+//   unit from the grid's CTAs that have not started yet, one issues the copies,
+//   one a tile's products, so that the next unit's copies and first S overlap the
+//   last one's end.
 //
 // Masked scores are -infinity and their P is 0, but 0 times an infinite or NaN
 // value is NaN: rows whose O is not finite although their sum is are computed
 // again by attend_row, which reads only what a row sees.  Values behind the
-// sequence's end, where there may be anything, become zeros before the product.
+// last sequence, where there may be anything, become zeros before the product.
 #pragma once
 
 #include "prompt_rows.cuh"
@@ -31,22 +40,39 @@ namespace dcp {
 namespace prompt {
 
 constexpr int kTileRows = 128;
+constexpr int kKeys = 128;      // a step
 constexpr float kBelow = 8.0f;  // a reference is set this far below the maximum
 constexpr float kMost = 15.0f;  // and holds until the maximum is this far above
+constexpr int kRing = 2;        // units on their way
 
 template <int D>
 struct Shape {
-  static constexpr int kTiles = D == 256 ? 1 : 2;    // of queries
-  static constexpr int kKeys = D == 256 ? 64 : 128;  // a step
-  static constexpr int kStages = D == 64 ? 8 : 4;    // of K or V of a step
-  static constexpr int kChunks = D / 64;             // of 64 elements, 128 bytes a row
+  static constexpr int kTiles = D == 256 ? 1 : 2;      // of queries
+  static constexpr bool kBeside = D != 128;            // P beside S
+  static constexpr int kPart = D < 128 ? D : 128;      // elements of a stage's rows
+  static constexpr int kParts = D / kPart;             // stages of a step's K, or V
+  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kChunks = D / 64;               // of 64 elements, 128 bytes a row
+  static constexpr int kPartChunks = kPart / 64;
   static constexpr int kQueryBytes = kTileRows * D * 2;
-  static constexpr int kStageBytes = kKeys * D * 2;
+  static constexpr int kStageBytes = kKeys * kPart * 2;
   static constexpr int kRowWarps = 4 * kTiles;
-  static constexpr int kThreads = 32 * (kRowWarps + 2);
-  static constexpr int kColumns = 512;  // of tensor memory: S of each tile, then O of each
-  static constexpr int kOut = kTiles * kKeys;
-  static_assert(kOut + kTiles * D <= kColumns, "");
+  static constexpr int kThreads = 32 * (kRowWarps + 4);
+  // columns of tensor memory
+  static constexpr int kColumns = 512;
+  static constexpr int kP = kBeside ? kTiles * kKeys : 0;
+  static constexpr int kPStep = kBeside ? kKeys / 2 : kKeys;
+  static constexpr int kOut = D == 64 ? 384 : 256;
+  static_assert(kOut + kTiles * D <= kColumns && (!kBeside || kP + kTiles * kPStep <= kOut), "");
+  // registers of the row warps and of the others: their sum is what the CTA is
+  // launched with (168 a thread)
+  static constexpr int kRowRegisters = 200, kOtherRegisters = 104;
+};
+
+struct Unit {
+  int first, n;  // its sequence
+  int q0;        // its first row there (-1: no more units)
+  int set;       // of heads
 };
 
 template <int D>
@@ -54,12 +80,18 @@ struct alignas(1024) Shared {
   using S = Shape<D>;
   uint8_t q[S::kTiles][S::kQueryBytes];
   uint8_t stage[S::kStages][S::kStageBytes];
-  float rows[S::kRowWarps][D];  // attend_row's
-  unsigned long long q_full, full[S::kStages], empty[S::kStages];
-  unsigned long long s_full[S::kTiles], p_ready[S::kTiles], o_full[S::kTiles], drained;
+  uint4 fetched;  // the next CTA's index, as the hardware reports it
+  unsigned long long fetch_done, drained[S::kTiles];
+  unsigned long long unit_full[kRing], unit_empty[kRing];
+  unsigned long long full[S::kStages], empty[S::kStages];
+  unsigned long long q_full[S::kTiles], q_empty[S::kTiles];
+  unsigned long long s_full[S::kTiles], s_read[S::kTiles];
+  unsigned long long p_ready[S::kTiles][2];
+  unsigned long long o_done[S::kTiles], o_read[S::kTiles];
+  unsigned long long turn[S::kTiles];
+  Unit unit[kRing];
   uint32_t tmem;
   int given_up;
-  int first, n, block;  // the unit: its sequence's first row and length, its block (-1: none)
 };
 
 struct TileParams {
@@ -68,56 +100,67 @@ struct TileParams {
   int packed;  // p: query heads of a tile's rows
   int tokens;  // of a tile
   int sets;    // of packed heads: kv_heads * group / packed
+  int sms;
   uint32_t q_bytes;  // of a tile's copy
 };
 
-// The u-th unit, those that lie furthest back in their sequences first, since
-// they see the most keys.  By one warp.
-template <int D>
-__device__ __forceinline__ void find_unit(const Params& p, int tokens, int u, Shared<D>& s) {
-  const int lane = threadIdx.x & 31;
-  auto blocks = [&](int b) {
+// Finds the u-th unit of the sequences (quickly where u grows from call to call);
+// those that
+// lie furthest back in their sequences come first, since they see the most
+// keys.  By one warp.
+struct Finder {
+  int level = -1;            // the block whose units are being taken
+  int behind = 0, here = 0;  // units of later blocks, and of this one
+  int base = 0, passed = 0;  // this block's units in the sequences before base
+
+  __device__ int blocks(const Params& p, int tokens, int b) const {
     if (b >= p.num_seqs) return 0;
     const int n = start_of(p, b + 1) - start_of(p, b);
     return n > 0 ? (n + tokens - 1) / tokens : 0;
-  };
-  int total = 0, most = 0;
-  for (int b = lane; b < p.num_seqs; b += 32) {
-    const int n = blocks(b);
-    total += n;
-    most = max(most, n);
   }
-  total = __reduce_add_sync(~0u, total);
-  most = __reduce_max_sync(~0u, most);
-  if (u >= total) {
-    if (lane == 0) s.block = -1;
-    return;
-  }
-  // the last block of which there are more than u, counting all behind it
-  int lo = 0, hi = most, behind = 0;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
+  // units whose block is `from` or later
+  __device__ int count(const Params& p, int tokens, int from) const {
     int c = 0;
-    for (int b = lane; b < p.num_seqs; b += 32) c += max(0, blocks(b) - mid);
-    c = __reduce_add_sync(~0u, c);
-    if (c > u) lo = mid; else hi = mid, behind = c;
+    for (int b = threadIdx.x & 31; b < p.num_seqs; b += 32)
+      c += max(0, blocks(p, tokens, b) - from);
+    return __reduce_add_sync(~0u, c);
   }
-  int left = u - behind;  // among the sequences that have block lo
-  for (int base = 0; base < p.num_seqs; base += 32) {
-    const unsigned has = __ballot_sync(~0u, blocks(base + lane) > lo);
-    const int c = __popc(has);
-    if (left < c) {
-      const int b = base + __fns(has, 0, left + 1);
-      if (lane == 0) {
-        s.first = start_of(p, b);
-        s.n = start_of(p, b + 1) - s.first;
-        s.block = lo;
+
+  __device__ Unit find(const Params& p, int tokens, int u) {
+    const int lane = threadIdx.x & 31;
+    if (u < behind + passed) *this = Finder();
+    if (level < 0 || u >= behind + here) {
+      int lo = 0, hi = level, at_hi = behind, at_lo;
+      if (level < 0) {
+        hi = 0;
+        for (int b = lane; b < p.num_seqs; b += 32) hi = max(hi, blocks(p, tokens, b));
+        hi = __reduce_max_sync(~0u, hi);
+      } else {
+        at_hi += here;
       }
-      return;
+      at_lo = count(p, tokens, 0);
+      if (u >= at_lo) return Unit{0, 0, -1, 0};
+      while (hi - lo > 1) {  // the last block with more than u units from it on
+        const int mid = (lo + hi) >> 1;
+        const int c = count(p, tokens, mid);
+        if (c > u) lo = mid, at_lo = c; else hi = mid, at_hi = c;
+      }
+      level = lo, behind = at_hi, here = at_lo - at_hi;
+      base = passed = 0;
     }
-    left -= c;
+    for (; base < p.num_seqs; base += 32) {
+      const unsigned has = __ballot_sync(~0u, blocks(p, tokens, base + lane) > level);
+      const int left = u - behind - passed;
+      if (left < __popc(has)) {
+        const int b = base + __fns(has, 0, left + 1);
+        const int first = start_of(p, b);
+        return Unit{first, start_of(p, b + 1) - first, level * tokens, 0};
+      }
+      passed += __popc(has);
+    }
+    return Unit{0, 0, -1, 0};
   }
-}
+};
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -145,11 +188,42 @@ __device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
   return d;
 }
 
+
 template <int D>
-__device__ __noinline__ void attend_row_again(const Params& p, int first, int n, int i, int h,
-                                              float* q_row) {
-  attend_row<D>(p, first, n, i, h, q_row);
+__device__ __noinline__ void attend_row_again(const Params& p, int first, int n, int i, int h) {
+  attend_row<D>(p, first, n, i, h);
 }
+
+// The three-input maximum.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// What all of a unit's warps derive from it.
+template <int D>
+struct Walk {
+  static constexpr int kTiles = Shape<D>::kTiles;
+  int head0, kv, from;
+  int steps[kTiles], most;
+
+  __device__ Walk(const TileParams& a, const Unit& u) {
+    const Params& p = a.p;
+    head0 = u.set * a.packed;
+    kv = head0 / p.group;
+    // the first key that a row of the unit sees, and each tile's steps from there
+    from = p.window ? max(0, u.q0 - p.window + 1) : 0;
+    most = 0;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int begin = u.q0 + t * a.tokens;
+      const int to = p.causal ? min(u.n, begin + a.tokens) : u.n;
+      steps[t] = begin < u.n ? (to - from + kKeys - 1) / kKeys : 0;
+      most = max(most, steps[t]);
+    }
+  }
+};
 
 template <int D, bool kHalf, bool kCapped>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
@@ -157,216 +231,454 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                  const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<D>;
-  constexpr int kKeys = Sh::kKeys, kTiles = Sh::kTiles, kStages = Sh::kStages;
+  constexpr int kTiles = Sh::kTiles, kStages = Sh::kStages, kParts = Sh::kParts;
   extern __shared__ uint8_t tiles_smem[];
   Shared<D>& s = *reinterpret_cast<Shared<D>*>(((uintptr_t)tiles_smem + 1023) & ~(uintptr_t)1023);
   const Params& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int set = blockIdx.x % a.sets;
-  const int span = kTiles * a.tokens;  // tokens of a unit
   kv4::grid_dependency_wait();
 
-  if (warp == 0) find_unit<D>(p, span, blockIdx.x / a.sets, s);
+  Finder finder;
+  if (warp == Sh::kRowWarps + 2) {
+    Unit u = finder.find(p, kTiles * a.tokens, blockIdx.x / a.sets);
+    u.set = blockIdx.x % a.sets;
+    if (lane == 0) s.unit[0] = u;
+  }
   if (warp == Sh::kRowWarps) {
     if (lane == 0) {
-      mbar_init(&s.q_full, 1);
-      mbar_init(&s.drained, 1);
-      for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
+      mbar_init(&s.fetch_done, 1);
+      for (int i = 0; i < kRing; ++i) {
+        mbar_init(&s.unit_full[i], 1);
+        mbar_init(&s.unit_empty[i], Sh::kRowWarps + kTiles + 1);
+      }
+      for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], kTiles);
       for (int t = 0; t < kTiles; ++t) {
+        mbar_init(&s.drained[t], 1);
+        mbar_init(&s.q_full[t], 1);
+        mbar_init(&s.q_empty[t], 1);
         mbar_init(&s.s_full[t], 1);
-        mbar_init(&s.p_ready[t], kTileRows);
-        mbar_init(&s.o_full[t], 1);
+        mbar_init(&s.s_read[t], 4);
+        mbar_init(&s.p_ready[t][0], 4);
+        mbar_init(&s.p_ready[t][1], 4);
+        mbar_init(&s.o_done[t], 1);
+        mbar_init(&s.o_read[t], 4);
+        mbar_init(&s.turn[t], 1);
       }
       s.given_up = 0;
       mbar_fence_init();
     }
     __syncwarp();
-    tmem_allocate(&s.tmem, Sh::kColumns);
   }
+  __syncthreads();
+  if (s.unit[0].q0 < 0) return;  // the grid has a CTA for as many units as there can be
+  if (warp == Sh::kRowWarps) tmem_allocate(&s.tmem, Sh::kColumns);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-
   const uint32_t tmem = s.tmem;
-  const int first = s.first, n = s.n, q0 = s.block * span;
-  if (s.block >= 0) {
-    const int head0 = set * a.packed, kv = head0 / p.group;
-    // the keys that the unit's rows see, and the steps of each tile over them
-    const int from = p.window ? max(0, q0 - p.window + 1) : 0;
-    int steps[kTiles], most = 0;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      const int begin = q0 + t * a.tokens;
-      const int to = p.causal ? min(n, begin + a.tokens) : n;
-      steps[t] = begin < n ? (to - from + kKeys - 1) / kKeys : 0;
-      most = max(most, steps[t]);
-    }
 
-    if (warp == Sh::kRowWarps + 1) {
-      // ------------------------------------------------------------- copies
-      if (lane == 0) {
-        int tiles = 0;
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) tiles += steps[t] > 0;
-        mbar_expect_tx(&s.q_full, tiles * a.q_bytes);
-        for (int t = 0; t < tiles; ++t)
-          for (int c = 0; c < Sh::kChunks; ++c)
-            tensor_load_3d(s.q[t] + c * kTileRows * 128, &q_map, c * 64, head0,
-                           first + q0 + t * a.tokens, &s.q_full);
-        int issued = 0;
-        for (int i = 0; i < 2 * most; ++i) {
-          const int slot = i % kStages, round = i / kStages;
-          if (round && !wait_for(&s.empty[slot], (round - 1) & 1, &s.given_up, a.status)) break;
-          mbar_expect_tx(&s.full[slot], Sh::kStageBytes);
-          for (int c = 0; c < Sh::kChunks; ++c)
-            tensor_load_3d(s.stage[slot] + c * kKeys * 128, i & 1 ? &v_map : &k_map, c * 64, kv,
-                           first + from + (i >> 1) * kKeys, &s.full[slot]);
-          ++issued;
-        }
-        if (s.given_up) {  // this thread's copies in flight, each for a limited time
-          mbar_wait_bounded(&s.q_full, 0, kPatience);
-          for (int i = max(0, issued - kStages); i < issued; ++i)
-            mbar_wait_bounded(&s.full[i % kStages], (i / kStages) & 1, kPatience);
-        }
-      }
-      __syncwarp();
-    } else if (warp == Sh::kRowWarps) {
-      // ----------------------------------------------------------- products
-      constexpr uint32_t kScores = mma_shape(!kHalf, kTileRows, kKeys, false, false);
-      constexpr uint32_t kOuts = mma_shape(!kHalf, kTileRows, D, false, true);
-      // a negative scale: negated queries
-      const uint32_t scores = kScores | (p.mult < 0.0f ? 1u << 13 : 0u);
-      auto wait = [&](unsigned long long* bar, uint32_t parity) {
-        const bool ok = wait_for(bar, parity, &s.given_up, a.status);
-        tmem_fence_after();
-        return __all_sync(~0u, ok);
-      };
-      auto multiply_scores = [&](int t, int slot) {
-        if (lane == 0) {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t in_chunk = (i & 3) * 32;
-            mma_smem(tmem + t * kKeys,
-                     rows_along_k(smem_u32(s.q[t]) + (i >> 2) * kTileRows * 128 + in_chunk),
-                     rows_along_k(smem_u32(s.stage[slot]) + (i >> 2) * kKeys * 128 + in_chunk),
-                     scores, i > 0);
+  // A wait of a whole warp.
+  auto wait = [&](unsigned long long* bar, uint32_t parity) {
+    return __all_sync(~0u, wait_for(bar, parity, &s.given_up, a.status)) != 0;
+  };
+  // The k-th unit.  All roles take all units, even when the CTA has given up.
+  auto unit_at = [&](int k, Unit* u) {
+    if (!mbar_wait_bounded(&s.unit_full[k % kRing], (k / kRing) & 1, 2 * kPatience))
+      return false;
+    *u = s.unit[k % kRing];
+    return u->q0 >= 0;
+  };
+  auto unit_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.unit_empty[k % kRing]);
+  };
+
+  if (warp >= Sh::kRowWarps) {
+    if constexpr (kTiles == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kOtherRegisters));
+    if (warp == Sh::kRowWarps + 2) {
+      // --------------------------------------------------------------- units
+      if (lane == 0) mbar_arrive(&s.unit_full[0]);
+      // No more are taken than the SMs cannot begin at once.
+      bool more = gridDim.x > (unsigned)a.sms;
+      for (int k = 1;; ++k) {
+        // whether the CTA has given up or not: what was taken has to be handed on
+        if (k >= kRing &&
+            !mbar_wait_bounded(&s.unit_empty[k % kRing], (k / kRing - 1) & 1, 2 * kPatience))
+          break;
+        Unit u{0, 0, -1, 0};
+        if (more && !s.given_up) {
+          uint32_t taken = 0, x = 0;
+          if (lane == 0) {
+            async_proxy_fence();
+            mbar_expect_tx(&s.fetch_done, 16);
+            asm volatile(
+                "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes."
+                "b128 [%0], [%1];" ::"r"(smem_u32(&s.fetched)),
+                "r"(smem_u32(&s.fetch_done))
+                : "memory");
           }
-          mma_commit(&s.s_full[t]);
+          __syncwarp();
+          if (wait(&s.fetch_done, (k - 1) & 1)) {
+            asm volatile(
+                "{\n .reg .pred p;\n .reg .b128 h;\n ld.shared.b128 h, [%2];\n"
+                " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+                " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+                " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
+                : "=r"(taken), "=r"(x)
+                : "r"(smem_u32(&s.fetched))
+                : "memory");
+          }
+          more = taken != 0;
+          if (taken) {
+            u = finder.find(p, kTiles * a.tokens, x / a.sets);
+            u.set = x % a.sets;
+          }
+        }
+        if (lane == 0) {
+          s.unit[k % kRing] = u;
+          mbar_arrive(&s.unit_full[k % kRing]);
         }
         __syncwarp();
-      };
-      bool ok = wait(&s.q_full, 0) && wait(&s.full[0], 0);
-      if (ok) {
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-          if (steps[t]) multiply_scores(t, 0);
-        if (lane == 0 && kStages < 2 * most) mma_commit(&s.empty[0]);
+        if (u.q0 < 0) break;
       }
-      for (int j = 0; ok && j < most; ++j) {
-        const int v_at = 2 * j + 1, k_at = 2 * j + 2;
-        const int v_slot = v_at % kStages, k_slot = k_at % kStages;
-        ok = wait(&s.full[v_slot], (v_at / kStages) & 1);
-        if (!ok) break;
-        const int inside = n - from - j * kKeys;  // keys of this step in the sequence
-        if (inside < kKeys) {
-          for (int i = lane; i < (kKeys - inside) * 8 * Sh::kChunks; i += 32) {
-            const int c = i / ((kKeys - inside) * 8), e = i - c * (kKeys - inside) * 8;
-            *reinterpret_cast<uint4*>(s.stage[v_slot] + c * kKeys * 128 + inside * 128 + e * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          async_proxy_fence();
-          __syncwarp();
-        }
-        bool next = false;
+    } else if (warp == Sh::kRowWarps + 1) {
+      // -------------------------------------------------------------- copies
+      int at = 0;  // stages filled
+      int q_round[kTiles] = {};
+      bool ok = true;
+      Unit u;
+      for (int k = 0; unit_at(k, &u); unit_done(k++)) {
+        if (!ok || lane != 0) continue;
+        const Walk<D> w(a, u);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-          if (j >= steps[t]) continue;
-          ok = ok && wait(&s.p_ready[t], j & 1);
+          if (!w.steps[t]) continue;
+          ok = ok && (q_round[t] == 0 || wait_for(&s.q_empty[t], (q_round[t] - 1) & 1, &s.given_up,
+                                                  a.status));
           if (!ok) break;
-          if (lane == 0) {
+          ++q_round[t];
+          mbar_expect_tx(&s.q_full[t], a.q_bytes);
+          for (int c = 0; c < Sh::kChunks; ++c)
+            tensor_load_3d(s.q[t] + c * kTileRows * 128, &q_map, c * 64, w.head0,
+                           u.first + u.q0 + t * a.tokens, &s.q_full[t]);
+        }
+        for (int i = 0; ok && i < 2 * w.most * kParts; ++i) {
+          const int slot = at % kStages, round = at / kStages;
+          ok = round == 0 || wait_for(&s.empty[slot], (round - 1) & 1, &s.given_up, a.status);
+          if (!ok) break;
+          ++at;
+          const int step = i / (2 * kParts), part = i % kParts;
+          mbar_expect_tx(&s.full[slot], Sh::kStageBytes);
+          for (int c = 0; c < Sh::kPartChunks; ++c)
+            tensor_load_3d(s.stage[slot] + c * kKeys * 128,
+                           i / kParts % 2 ? &v_map : &k_map, (part * Sh::kPartChunks + c) * 64,
+                           w.kv, u.first + w.from + step * kKeys, &s.full[slot]);
+        }
+      }
+      if (lane == 0 && s.given_up) {  // copies in flight, each for a limited time
 #pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-              mma_tmem(tmem + Sh::kOut + t * D, tmem + t * kKeys + i * 8,
-                       rows_across_k(smem_u32(s.stage[v_slot]) + i * 2048, kKeys * 128), kOuts,
-                       j > 0 || i > 0);
-          }
-          __syncwarp();
-          if (j + 1 < steps[t]) {
-            if (!next) ok = wait(&s.full[k_slot], (k_at / kStages) & 1);
-            next = true;
-            if (!ok) break;
-            multiply_scores(t, k_slot);
-          } else if (lane == 0) {
-            mma_commit(&s.o_full[t]);
-          }
-        }
-        if (ok && lane == 0) {
-          if (v_at + kStages < 2 * most) mma_commit(&s.empty[v_slot]);
-          if (next && k_at + kStages < 2 * most) mma_commit(&s.empty[k_slot]);
-        }
-        __syncwarp();
+        for (int t = 0; t < kTiles; ++t)
+          if (q_round[t]) mbar_wait_bounded(&s.q_full[t], (q_round[t] - 1) & 1, kPatience);
+        for (int i = max(0, at - kStages); i < at; ++i)
+          mbar_wait_bounded(&s.full[i % kStages], (i / kStages) & 1, kPatience);
       }
-      if (!ok) {  // the products in flight, for a limited time
-        if (lane == 0) {
-          mma_commit(&s.drained);
-          mbar_wait_bounded(&s.drained, 0, kPatience);
+      __syncwarp();
+    } else if (warp == Sh::kRowWarps || (kTiles == 2 && warp == Sh::kRowWarps + 3)) {
+      // ------------------------------------------------------------ products
+      // A warp for each tile, so that one's waits pass while the other's products
+      // run.  What a warp does between two products is time in which the tensor
+      // cores may run dry, so all that it computes is the same in all lanes, and
+      // written so that the compiler sees it: descriptors then stay in uniform
+      // registers, from which the instruction takes them.  From others an
+      // instruction took 87 cycles to issue, more than the 64 it takes to run.
+      const int t = same_in_all(warp == Sh::kRowWarps ? 0 : 1);
+      const bool leader = elect_one();
+      // a negative scale: negated queries
+      const uint32_t scores =
+          mma_shape(!kHalf, kTileRows, kKeys, false, false) | (p.mult < 0.0f ? 1u << 13 : 0u);
+      constexpr uint32_t kOuts = mma_shape(!kHalf, kTileRows, Sh::kPart, false, true);
+      constexpr uint32_t kStageStep = Sh::kStageBytes / 16;  // in descriptors
+      const uint32_t tm = same_in_all(tmem);
+      const uint32_t s_at = tm + t * kKeys, p_at = tm + Sh::kP + t * Sh::kPStep;
+      const uint32_t o_at = tm + Sh::kOut + t * D;
+      const uint64_t q_rows = rows_along_k(same_in_all(smem_u32(s.q[t])));
+      const uint64_t k_rows = rows_along_k(same_in_all(smem_u32(s.stage[0])));
+      const uint64_t v_rows = rows_across_k(same_in_all(smem_u32(s.stage[0])), kKeys * 128);
+      // the ring's next stages: kParts of them with their phase
+      int slot = 0;
+      uint32_t phase = 0;
+      struct Stages {
+        int slot[kParts];
+        uint32_t phase[kParts];
+      };
+      auto take = [&] {
+        Stages g;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          g.slot[i] = slot, g.phase[i] = phase;
+          if (++slot == kStages) slot = 0, phase ^= 1;
         }
-        __syncwarp();
-      }
-    } else {
-      // --------------------------------------------------------------- rows
-      const int t = warp >> 2;
-      const int row = 32 * (warp & 3) + lane;
-      const int token = row / a.packed;
-      const int i = q0 + t * a.tokens + token, head = head0 + row - token * a.packed;
-      const bool valid = token < a.tokens && i < n;
-      // the keys that the row sees, counted from the first step's first
-      const int lo = valid && p.window ? max(0, i - p.window + 1) - from : 0;
-      const int hi = valid ? (p.causal ? i + 1 : n) - from : INT32_MAX;
-      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-      const uint32_t s_at = tmem + lanes + t * kKeys;
-      const uint32_t o_at = tmem + lanes + Sh::kOut + t * D;
-      const float mult = fabsf(p.mult), late = kCapped ? 1.0f : mult;
-      float ref = -INFINITY, l = 0.0f, over = 0.0f;  // over: what l is too large by
+        return g;
+      };
+      auto arrived = [&](const Stages& g) {
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) ok = ok && wait(&s.full[g.slot[i]], g.phase[i]);
+        return ok;
+      };
+      auto free = [&](const Stages& g) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          if (leader) mma_commit(&s.empty[g.slot[i]]);
+      };
+      // P over S: the tiles' products take turns, a whole step each, so that one's
+      // run while the other's rows are exponentiated (mixed they took 3700 cycles a
+      // step of both tiles, both of whose rows then waited at the same time).  The
+      // turn is passed on half way through the scores: it takes about as long to
+      // arrive as the rest of them to run.
+      constexpr bool kTurns = !Sh::kBeside;
+      uint32_t turns = 0;
+      auto my_turn = [&] { return wait(&s.turn[t], (turns & 1) ^ (t == 0)); };
+      auto next_turn = [&] {
+        if (leader) mbar_arrive(&s.turn[kTiles - 1 - t]);
+        ++turns;
+      };
+      // S from g; `last`: of the unit
+      auto multiply_scores = [&](const Stages& g, bool last, bool pass) {
+        tmem_fence_after();
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          const uint64_t rows = k_rows + g.slot[part] * kStageStep;
+#pragma unroll
+          for (int i = 0; i < Sh::kPart / 16; ++i) {
+            if (kTurns && pass && i == D / 32) next_turn();
+            if (leader)
+              mma_smem(s_at,
+                       q_rows + ((part * Sh::kPartChunks + i / 4) * kTileRows * 128 + i % 4 * 32) / 16,
+                       rows + (i / 4 * kKeys * 128 + i % 4 * 32) / 16, scores, part > 0 || i > 0);
+          }
+        }
+        if (leader) mma_commit(&s.s_full[t]);
+        if (last && leader) mma_commit(&s.q_empty[t]);
+      };
+      uint32_t q_round = 0, s_round = 0;  // units and steps of this tile
       bool ok = true;
-      const int my_steps = t == 0 ? steps[0] : steps[kTiles - 1];
-      for (int j = 0; j < my_steps; ++j) {
-        ok = wait_for(&s.s_full[t], j & 1, &s.given_up, a.status);
-        ok = __all_sync(~0u, ok);
+      const int rows_end = same_in_all(start_of(p, p.num_seqs));
+      Unit u;
+      for (int k = 0; unit_at(k, &u); unit_done(k++)) {
+        if (!ok) continue;
+        u = Unit{same_in_all(u.first), same_in_all(u.n), same_in_all(u.q0), same_in_all(u.set)};
+        const Walk<D> w(a, u);
+        const int steps = t == 0 ? w.steps[0] : w.steps[kTiles - 1];
+        // the first step's scores, then each step's next ones and its products
+        // with the values; stages that only the other tile needs are passed on
+        const Stages first_k = take();
+        ok = arrived(first_k);
+        if (steps > 0) {
+          ok = ok && wait(&s.q_full[t], q_round & 1) &&
+               (!Sh::kBeside || s_round == 0 || wait(&s.s_read[t], (s_round - 1) & 1));
+          if (ok) multiply_scores(first_k, steps == 1, false);
+        }
+        if (!ok) continue;
+        free(first_k);
+        for (int j = 0; ok && j < w.most; ++j) {
+          const Stages v_at = take();
+          Stages k_at{};
+          const bool next = j + 1 < w.most;
+          if (next) k_at = take();
+          auto next_scores = [&] {
+            if (!kTurns || j >= steps) ok = arrived(k_at);
+            if (j + 1 < steps) {
+              if (Sh::kBeside) ok = ok && wait(&s.s_read[t], s_round & 1);
+              if (ok) multiply_scores(k_at, j + 2 == steps, true);
+            } else if constexpr (kTurns) {
+              next_turn();
+            }
+          };
+          if (Sh::kBeside && next) next_scores();
+          ok = ok && arrived(v_at);
+          if (!ok) break;
+          if (j < steps) {
+            // rows of this step behind the last sequence
+            const int inside = rows_end - u.first - w.from - j * kKeys;
+            if (inside < kKeys) {
+              for (int c = 0; c < Sh::kChunks; ++c)
+                for (int i = inside * 8 + lane; i < kKeys * 8; i += 32)
+                  *reinterpret_cast<uint4*>(s.stage[v_at.slot[c / Sh::kPartChunks]] +
+                                            c % Sh::kPartChunks * kKeys * 128 + i * 16) =
+                      make_uint4(0, 0, 0, 0);
+              async_proxy_fence();
+              __syncwarp();
+            }
+            if (j == 0 && q_round > 0) ok = wait(&s.o_read[t], (q_round - 1) & 1);
+            if constexpr (kTurns) {
+              ok = ok && wait(&s.p_ready[t][0], s_round & 1) &&
+                   wait(&s.p_ready[t][1], s_round & 1) && (!next || arrived(k_at)) && my_turn();
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if constexpr (!kTurns) ok = ok && wait(&s.p_ready[t][h], s_round & 1);
+              if (!ok) break;
+              tmem_fence_after();
+#pragma unroll
+              for (int part = 0; part < kParts; ++part) {
+                const uint64_t rows = v_rows + v_at.slot[part] * kStageStep;
+#pragma unroll
+                for (int i = h * kKeys / 32; i < (h + 1) * kKeys / 32; ++i)
+                  if (leader)
+                    mma_tmem(o_at + part * Sh::kPart, p_at + i * 8, rows + i * 2048 / 16, kOuts,
+                             i > 0 || j > 0);
+              }
+            }
+            if (!ok) break;
+            if ((Sh::kBeside || j + 1 == steps) && leader) mma_commit(&s.o_done[t]);
+            ++s_round;
+          } else if constexpr (kTurns) {
+            ok = my_turn();
+          }
+          if (!ok) break;
+          if (!Sh::kBeside && next) next_scores();
+          if (kTurns && !next) next_turn();
+          free(v_at);
+          if (next) free(k_at);
+        }
+        q_round += steps > 0;
+      }
+      // products in flight, and the arrivals that they owe, for a limited time
+      if (leader) mma_commit(&s.drained[t]);
+      mbar_wait_bounded(&s.drained[t], 0, kPatience);
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ rows
+    if constexpr (kTiles == 2)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRowRegisters));
+    const int t = warp >> 2;
+    const int row = 32 * (warp & 3) + lane;
+    const int token = row / a.packed;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_at = tmem + lanes + t * kKeys;
+    const uint32_t p_at = tmem + lanes + Sh::kP + t * Sh::kPStep;
+    const uint32_t o_at = tmem + lanes + Sh::kOut + t * D;
+    const float mult = fabsf(p.mult), late = kCapped ? 1.0f : mult;
+    auto arrive = [&](unsigned long long* bar) {
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    int s_round = 0, o_round = 0;  // phases of s_full and o_done
+    bool ok = true;
+    Unit u;
+    for (int k = 0; unit_at(k, &u); unit_done(k++)) {
+      const Walk<D> w(a, u);
+      const int steps = t == 0 ? w.steps[0] : w.steps[kTiles - 1];
+      if (steps == 0) continue;
+      const int i = u.q0 + t * a.tokens + token, head = w.head0 + row - token * a.packed;
+      const bool valid = token < a.tokens && i < u.n;
+      // the keys that the row sees, counted from the first step's first
+      const int lo = valid && p.window ? max(0, i - p.window + 1) - w.from : 0;
+      const int hi = valid ? (p.causal ? i + 1 : u.n) - w.from : INT32_MAX;
+      const int some_lo = __reduce_max_sync(~0u, lo), some_hi = __reduce_min_sync(~0u, hi);
+      float ref = -INFINITY, l = 0.0f, over = 0.0f;  // over: what l is too large by
+      for (int j = 0; ok && j < steps; ++j) {
+        ok = wait(&s.s_full[t], s_round & 1);
         if (!ok) break;
+        ++s_round;
         tmem_fence_after();
         uint32_t raw[kKeys];
-#pragma unroll
-        for (int c = 0; c < kKeys / 64; ++c) tmem_load64(s_at + 64 * c, raw + 64 * c);
         float* x = reinterpret_cast<float*>(raw);
-        if constexpr (kCapped) {
-#pragma unroll
-          for (int e = 0; e < kKeys; ++e) x[e] = p.cap * kv4::tanh_score(x[e] * mult);
-        }
         const int base = j * kKeys;
-        if (__any_sync(~0u, base < lo || base + kKeys > hi)) {
+        auto cap_scores = [&] {
+          if constexpr (kCapped) {
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e) x[e] = p.cap * kv4::tanh_score(x[e] * mult);
+          }
+        };
+        auto maximum = [&](int h) {
+          float m[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f) m[f] = fmaxf(x[64 * h + f], x[64 * h + f + 4]);
+#pragma unroll
+          for (int e = 64 * h + 8; e < 64 * h + 64; e += 8)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) m[f] = max3(m[f], x[e + f], x[e + f + 4]);
+          return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+        };
+        // P of a half, in place, and its sum
+        auto exponentials = [&](int h) {
+          const float less = ref == -INFINITY ? 0.0f : -ref;
+          float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            float2 y = fma2(make_float2(x[64 * h + e], x[64 * h + e + 1]), make_float2(late, late),
+                            make_float2(less, less));
+            y.x = kv4::exp2_approx(y.x);
+            y.y = kv4::exp2_approx(y.y);
+            sum[e / 2 & 1] = add2(sum[e / 2 & 1], y);
+            raw[64 * h + e / 2] = round_pair<kHalf>(y.x, y.y);
+          }
+          const float2 both = add2(sum[0], sum[1]);
+          return both.x + both.y;
+        };
+        // P beside S: the last product may still be reading it, and adding to O.
+        // P over S: this step's S came after it.
+        bool last_done = !Sh::kBeside || j == 0;
+        auto wait_last = [&] {
+          if (!last_done) {
+            ok = wait(&s.o_done[t], o_round++ & 1);
+            tmem_fence_after();
+          }
+          last_done = true;
+        };
+        // What follows the first half's exponentials.
+        auto hand_over = [&](float sum) {
+          if constexpr (Sh::kBeside) arrive(&s.s_read[t]);
+          wait_last();
+          if (!ok) return sum;
+          tmem_store32(p_at, raw);
+          tmem_wait_store();
+          arrive(&s.p_ready[t][0]);
+          sum += exponentials(1);
+          tmem_store32(p_at + 32, raw + 64);
+          tmem_wait_store();
+          arrive(&s.p_ready[t][1]);
+          return sum;
+        };
+
+        // Most steps leave the reference where it is, and have nothing to mask.
+        // Their first half is exponentiated with it before the maximum is known: a
+        // sum up to 2^15 says that it was good, as does the second half's maximum,
+        // which is found beside the exponentials.
+        float sum = 0.0f;
+        bool done = false;
+        if (__builtin_expect(j > 0 && base >= some_lo && base + kKeys <= some_hi, 1)) {
+          tmem_load128(s_at, raw);
+          cap_scores();
+          sum = exponentials(0);
+          const bool good = sum <= 32768.0f && maximum(1) * late <= ref + kMost && ref > -INFINITY;
+          done = __all_sync(~0u, good);
+          if (__builtin_expect(done, 1)) sum = hand_over(sum);
+        }
+        if (__builtin_expect(!done, 0)) {
+          tmem_load128(s_at, raw);
+          cap_scores();
 #pragma unroll
           for (int e = 0; e < kKeys; ++e)
             if (base + e < lo || base + e >= hi) x[e] = -INFINITY;
-        }
-        float top4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int e = 4; e < kKeys; e += 4)
-#pragma unroll
-          for (int f = 0; f < 4; ++f) top4[f] = fmaxf(top4[f], x[e + f]);
-        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * late;
-        const bool moves = top > ref + kMost;
-        if (__any_sync(~0u, moves)) {
+          const float top = fmaxf(maximum(0), maximum(1)) * late;
+          const bool moves = j == 0 || top > ref + kMost;
           float shrink = 1.0f;
-          if (moves) {
+          if (moves && top > ref) {
             const float next = top - kBelow;
             shrink = exp2f(ref - next);  // 0 at first
             ref = next;
             l *= shrink;
             over *= shrink;
           }
-          // S of this step came after the products with the last one's P
-          if (j > 0) {
+          if (j > 0 && __any_sync(~0u, moves)) {
+            wait_last();
+            if (!ok) break;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -377,67 +689,45 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
               tmem_store32(o_at + c, o);
             }
           }
+          sum = hand_over(exponentials(0));
         }
-        const float less = ref == -INFINITY ? 0.0f : -ref;
-        float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 64) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            float2 y = fma2(make_float2(x[c + e], x[c + e + 1]), make_float2(late, late),
-                            make_float2(less, less));
-            y.x = kv4::exp2_approx(y.x);
-            y.y = kv4::exp2_approx(y.y);
-            sum[e / 2 & 1] = add2(sum[e / 2 & 1], y);
-            w[e / 2] = round_pair<kHalf>(y.x, y.y);
-          }
-          tmem_store32(s_at + c / 2, w);
-        }
-        tmem_wait_store();
-        tmem_fence_before();
-        mbar_arrive(&s.p_ready[t]);
-        const float2 both = add2(sum[0], sum[1]);
-        const float add = both.x + both.y - over, now = l + add;
+        if (!ok) break;
+        const float add = sum - over, now = l + add;
         over = (now - l) - add;
         l = now;
       }
-      if (my_steps > 0) {
-        ok = ok && wait_for(&s.o_full[t], 0, &s.given_up, a.status);
-        ok = __all_sync(~0u, ok);
-        tmem_fence_after();
-        const float inverse = ok ? (l == 0.0f ? 0.0f : 1.0f / l) : NAN;
-        const int64_t out_row = (int64_t)(first + i) * p.q_heads + head;
-        bool finite = true;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_load32(o_at + c, o);
-          uint32_t w[16];
+      ok = ok && wait(&s.o_done[t], o_round & 1);
+      ++o_round;
+      tmem_fence_after();
+      const float inverse = ok ? (l == 0.0f ? 0.0f : 1.0f / l) : NAN;
+      const int64_t out_row = (int64_t)(u.first + i) * p.q_heads + head;
+      bool finite = true;
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float y0 = __uint_as_float(o[e]), y1 = __uint_as_float(o[e + 1]);
+      for (int c = 0; c < D; c += 64) {
+        uint32_t o[64];
+        tmem_load64(o_at + c, o);
+        if (c + 64 == D) arrive(&s.o_read[t]);
+#pragma unroll
+        for (int b = 0; b < 64; b += 8) {
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float y0 = __uint_as_float(o[b + e]), y1 = __uint_as_float(o[b + e + 1]);
             finite = finite && fabsf(y0) <= 3.4028234e38f && fabsf(y1) <= 3.4028234e38f;
-            w[e / 2] = round_pair<kHalf>(y0 * inverse, y1 * inverse);
+            y[e / 2] = round_pair<kHalf>(y0 * inverse, y1 * inverse);
           }
-          if (valid) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
-                                                 (out_row * D + c) * 2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              to[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-          }
+          if (valid)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (out_row * D + c + b) * 2) =
+                make_uint4(y[0], y[1], y[2], y[3]);
         }
-        if (valid)
-          p.lse[out_row] = !ok ? NAN : l == 0.0f ? -INFINITY : kLn2 * (ref + log2f(l));
-        // a NaN among the scores that the row sees makes the sum NaN, and is right
-        unsigned again = __ballot_sync(~0u, ok && valid && !finite && l == l);
-        while (again) {
-          const int at = __ffs(again) - 1;
-          again &= again - 1;
-          attend_row_again<D>(p, first, n, __shfl_sync(~0u, i, at), __shfl_sync(~0u, head, at),
-                              s.rows[warp]);
-        }
+      }
+      if (valid) p.lse[out_row] = !ok ? NAN : l == 0.0f ? -INFINITY : kLn2 * (ref + log2f(l));
+      // a NaN among the scores that the row sees makes the sum NaN, and is right
+      unsigned again = __ballot_sync(~0u, ok && valid && !finite && l == l);
+      while (again) {
+        const int r = __ffs(again) - 1;
+        again &= again - 1;
+        attend_row_again<D>(p, u.first, u.n, __shfl_sync(~0u, i, r), __shfl_sync(~0u, head, r));
       }
     }
   }

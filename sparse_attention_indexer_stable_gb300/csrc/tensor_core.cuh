@@ -64,6 +64,26 @@ __device__ __forceinline__ void tmem_load64(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_load128(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "{\n .reg .b32 a, b;\n mov.b32 a, %128;\n add.u32 b, %128, 64;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, "
+      "%34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, "
+      "%50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [a];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+      "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+      "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, "
+      "%110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, "
+      "%124, %125, %126, %127}, [b];\n"
+      " tcgen05.wait::ld.sync.aligned;\n}"
+      : DCP_R16(r, 0), DCP_R16(r, 16), DCP_R16(r, 32), DCP_R16(r, 48), DCP_R16(r, 64),
+        DCP_R16(r, 80), DCP_R16(r, 96), DCP_R16(r, 112)
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -122,6 +142,19 @@ __device__ __forceinline__ void mma_commit(unsigned long long* bar) {
       : "memory");
 }
 
+// One lane of a warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(r));
+  return r != 0;
+}
+// x of lane 0: a value that the compiler knows to be the same in all lanes.
+template <typename T>
+__device__ __forceinline__ T same_in_all(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // ------------------------------------------------------------ tensor copies
 __device__ __forceinline__ void tensor_load_3d(void* dst, const CUtensorMap* map, int x, int y,
                                                int z, unsigned long long* bar) {
@@ -141,7 +174,7 @@ __device__ __forceinline__ void async_proxy_fence() {
 // and the device's status bit; all later ones end at once.
 constexpr unsigned long long kPatience = 2000000000ull;  // SM clocks
 
-__device__ __noinline__ bool wait_long(unsigned long long* bar, uint32_t parity,
+__device__ __forceinline__ bool wait_long(unsigned long long* bar, uint32_t parity,
                                        volatile int* given_up, unsigned int* status) {
   const unsigned long long t0 = clock64();
   for (;;) {

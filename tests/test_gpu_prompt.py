@@ -283,6 +283,15 @@ def test_many_short_sequences(dk):
     assert torch.isfinite(out.float()).all()
 
 
+@pytest.mark.parametrize("dim,heads,group", [(64, 8, 1), (128, 8, 8), (256, 4, 2)])
+def test_more_work_than_the_gpu_holds(dk, dim, heads, group):
+    """Every CTA takes several units, of all lengths."""
+    lens = [1100, 3, 260, 700, 0, 41, 900, 129, 513]
+    q, k, v = inputs(21, sum(lens), heads, group, dim, "bf16")
+    check(dk, q, k, v, bounds(lens), "bf16")
+    check(dk, q, k, v, bounds(lens), "bf16", window=200)
+
+
 def test_nothing_to_do(dk):
     q = torch.empty((0, 8, 64), dtype=torch.bfloat16, device=DEV)
     k = torch.empty((0, 2, 64), dtype=torch.bfloat16, device=DEV)

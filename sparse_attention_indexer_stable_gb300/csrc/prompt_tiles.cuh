@@ -9,10 +9,11 @@
 //
 // A tile's rows are p query heads that share the key/value head times 128 / p
 // tokens, so that a short prompt still fills the tile and the diagonal cuts off
-// little.  ref is a reference that follows the row's maximum: set 2^8 below it,
-// and moved (O and l multiplied by the difference) only once the maximum has
-// passed it by 2^15, so that O is rarely read before the end.  P stays below
-// fp16's 65504, and fp16's smallest step, 2^-24, is 2^-32 of the largest P.
+// little.  ref is a reference that follows the row's maximum and stands while P
+// fits its type, so that O is rarely read before the end:
+// - fp16: set 2^4 below the maximum, until P passes 2^15 (of 65504); fp16's
+//   smallest step, 2^-24, is then 2^-28 of the largest P or less.
+// - bf16, which has fp32's range: set at the maximum, until P passes 2^60.
 //
 // What bounds a step is the tensor cores' time for both products, or, for heads
 // of 64, the exponentials; the rest has to happen meanwhile:
@@ -41,8 +42,6 @@ namespace prompt {
 
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;      // a step
-constexpr float kBelow = 8.0f;  // a reference is set this far below the maximum
-constexpr float kMost = 15.0f;  // and holds until the maximum is this far above
 constexpr int kRing = 2;        // units on their way
 
 template <int D>
@@ -562,6 +561,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const uint32_t p_at = tmem + lanes + Sh::kP + t * Sh::kPStep;
     const uint32_t o_at = tmem + lanes + Sh::kOut + t * D;
     const float mult = fabsf(p.mult), late = kCapped ? 1.0f : mult;
+    // how far below the maximum a reference is set, how far above it the maximum
+    // may go before it is set anew, and the sum of half a step's P up to which
+    // none is too large
+    constexpr float kBelow = kHalf ? 4.0f : 0.0f, kMost = kHalf ? 15.0f : 60.0f;
+    constexpr float kLargest = kHalf ? 0x1p15f : 0x1p60f;
     auto arrive = [&](unsigned long long* bar) {
       tmem_fence_before();
       __syncwarp();
@@ -589,11 +593,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         uint32_t raw[kKeys];
         float* x = reinterpret_cast<float*>(raw);
         const int base = j * kKeys;
-        auto cap_scores = [&] {
+        auto cap_scores = [&](int h) {
           if constexpr (kCapped) {
 #pragma unroll
-            for (int e = 0; e < kKeys; ++e) x[e] = p.cap * kv4::tanh_score(x[e] * mult);
+            for (int e = 64 * h; e < 64 * h + 64; ++e) x[e] = p.cap * kv4::tanh_score(x[e] * mult);
           }
+        };
+        auto mask = [&](int h) {
+#pragma unroll
+          for (int e = 64 * h; e < 64 * h + 64; ++e)
+            if (base + e < lo || base + e >= hi) x[e] = -INFINITY;
         };
         auto maximum = [&](int h) {
           float m[4];
@@ -631,52 +640,38 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           }
           last_done = true;
         };
-        // What follows the first half's exponentials.
-        auto hand_over = [&](float sum) {
-          if constexpr (Sh::kBeside) arrive(&s.s_read[t]);
-          wait_last();
-          if (!ok) return sum;
-          tmem_store32(p_at, raw);
-          tmem_wait_store();
-          arrive(&s.p_ready[t][0]);
-          sum += exponentials(1);
-          tmem_store32(p_at + 32, raw + 64);
-          tmem_wait_store();
-          arrive(&s.p_ready[t][1]);
-          return sum;
-        };
-
-        // Most steps leave the reference where it is, and have nothing to mask.
-        // Their first half is exponentiated with it before the maximum is known: a
-        // sum up to 2^15 says that it was good, as does the second half's maximum,
-        // which is found beside the exponentials.
+        // Most steps leave the reference where it is.  So the first half is
+        // exponentiated with it before its maximum is known: its sum says whether
+        // it was good, as does the second half's maximum, which is found beside the
+        // exponentials.  What most steps do not do stands apart, so that they run
+        // straight through their instructions.
+        tmem_load128(s_at, raw);
+        cap_scores(0);
+        cap_scores(1);
+        const bool edge = base < some_lo || base + kKeys > some_hi;
+        if (__builtin_expect(edge, 0)) mask(0), mask(1);
         float sum = 0.0f;
-        bool done = false;
-        if (__builtin_expect(j > 0 && base >= some_lo && base + kKeys <= some_hi, 1)) {
-          tmem_load128(s_at, raw);
-          cap_scores();
+        bool good = false;
+        if (__builtin_expect(j > 0, 1)) {
           sum = exponentials(0);
-          const bool good = sum <= 32768.0f && maximum(1) * late <= ref + kMost && ref > -INFINITY;
-          done = __all_sync(~0u, good);
-          if (__builtin_expect(done, 1)) sum = hand_over(sum);
+          good = sum <= kLargest && maximum(1) * late <= ref + kMost && ref > -INFINITY;
         }
-        if (__builtin_expect(!done, 0)) {
-          tmem_load128(s_at, raw);
-          cap_scores();
-#pragma unroll
-          for (int e = 0; e < kKeys; ++e)
-            if (base + e < lo || base + e >= hi) x[e] = -INFINITY;
+        if (__builtin_expect(!__all_sync(~0u, good), 0)) {
+          if (j > 0) {
+            tmem_load64(s_at, raw);
+            cap_scores(0);
+            if (edge) mask(0);
+          }
           const float top = fmaxf(maximum(0), maximum(1)) * late;
-          const bool moves = j == 0 || top > ref + kMost;
           float shrink = 1.0f;
-          if (moves && top > ref) {
+          if (!good && top > ref + kBelow) {
             const float next = top - kBelow;
             shrink = exp2f(ref - next);  // 0 at first
             ref = next;
             l *= shrink;
             over *= shrink;
           }
-          if (j > 0 && __any_sync(~0u, moves)) {
+          if (j > 0) {
             wait_last();
             if (!ok) break;
 #pragma unroll 1
@@ -689,9 +684,18 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
               tmem_store32(o_at + c, o);
             }
           }
-          sum = hand_over(exponentials(0));
+          sum = exponentials(0);
         }
+        if constexpr (Sh::kBeside) arrive(&s.s_read[t]);
+        wait_last();
         if (!ok) break;
+        tmem_store32(p_at, raw);
+        tmem_wait_store();
+        arrive(&s.p_ready[t][0]);
+        sum += exponentials(1);
+        tmem_store32(p_at + 32, raw + 64);
+        tmem_wait_store();
+        arrive(&s.p_ready[t][1]);
         const float add = sum - over, now = l + add;
         over = (now - l) - add;
         l = now;

@@ -20,8 +20,8 @@ def attention(q, k, v, starts, *, causal=True, window=0, scale=None, softcap=0.0
     - the sum of the probabilities: 128 roundings of 2^-24 along the longest
       chain of a tile, and the tiles' sum compensated;
     - the second product: p_step, and n / 16 accumulations that may cut off a
-      bit of 2^-23; fp16 probabilities against a reference of 2^7 or more below
-      the type's smallest step 2^-25, 2^-32 each;
+      bit of 2^-23; fp16 probabilities below the smallest normal one are off by
+      half a smallest step, 2^-25, where the largest is at least 2^4: 2^-29 each;
     - the output's rounding to its type is added by the caller."""
     import torch
 
@@ -61,7 +61,7 @@ def attention(q, k, v, starts, *, causal=True, window=0, scale=None, softcap=0.0
             rel = torch.expm1(2 * dx) + sums
             size = p @ vv.abs()
             tol[a:b, h] = size * (p_step * (1 + 2.0 ** -6) + rel + (seen / 16 + 32) * 2.0 ** -23
-                                  )[:, None] + (seen * 2.0 ** -32)[:, None] * vv.abs().amax()
+                                  )[:, None] + (seen * 2.0 ** -29)[:, None] * vv.abs().amax()
             lse_tol[a:b, h] = dx + sums + 2.0 ** -21 * (1 + e.abs())
     return out, lse, tol, lse_tol
 

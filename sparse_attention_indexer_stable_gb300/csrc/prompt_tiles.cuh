@@ -50,7 +50,7 @@ struct Shape {
   static constexpr bool kBeside = D != 128;            // P beside S
   static constexpr int kPart = D < 128 ? D : 128;      // elements of a stage's rows
   static constexpr int kParts = D / kPart;             // stages of a step's K, or V
-  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kStages = D == 64 ? 8 : 4;
   static constexpr int kChunks = D / 64;               // of 64 elements, 128 bytes a row
   static constexpr int kPartChunks = kPart / 64;
   static constexpr int kQueryBytes = kTileRows * D * 2;
@@ -79,6 +79,7 @@ struct alignas(1024) Shared {
   using S = Shape<D>;
   uint8_t q[S::kTiles][S::kQueryBytes];
   uint8_t stage[S::kStages][S::kStageBytes];
+  uint4 rows[S::kRowWarps][32][8];  // of 64 outputs on their way to memory
   uint4 fetched;  // the next CTA's index, as the hardware reports it
   unsigned long long fetch_done, drained[S::kTiles];
   unsigned long long unit_full[kRing], unit_empty[kRing];
@@ -169,6 +170,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         "l"(reinterpret_cast<uint64_t&>(c)));
   return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("add.rn.f32x2 %0, %1, %2;"
@@ -199,6 +207,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+
+// tanh(u) / u as a polynomial in u^2 for |u| <= 1, relative error below 2^-20.5
+// (weighted least squares iterated towards equal extremes).
+constexpr int kTanhTerms = 6;
+__device__ constexpr float kTanh[kTanhTerms] = {0x1.ffffecp-1f,  -0x1.554a16p-2f, 0x1.1000f8p-3f,
+                                                -0x1.a6c0f2p-5f, 0x1.1251b8p-6f,  -0x1.920176p-9f};
 
 // What all of a unit's warps derive from it.
 template <int D>
@@ -431,11 +445,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         for (int i = 0; i < kParts; ++i)
           if (leader) mma_commit(&s.empty[g.slot[i]]);
       };
-      // P over S: the tiles' products take turns, a whole step each, so that one's
-      // run while the other's rows are exponentiated (mixed they took 3700 cycles a
-      // step of both tiles, both of whose rows then waited at the same time).  The
-      // turn is passed on half way through the scores: it takes about as long to
-      // arrive as the rest of them to run.
+      // P over S: the tiles' products take turns, so that each tile's next S comes
+      // soon (mixed they took 3700 cycles a step of both tiles).  A turn begins
+      // with P's second half; the first half's product needs none.
       constexpr bool kTurns = !Sh::kBeside;
       uint32_t turns = 0;
       auto my_turn = [&] { return wait(&s.turn[t], (turns & 1) ^ (t == 0)); };
@@ -451,7 +463,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           const uint64_t rows = k_rows + g.slot[part] * kStageStep;
 #pragma unroll
           for (int i = 0; i < Sh::kPart / 16; ++i) {
-            if (kTurns && pass && i == D / 32) next_turn();
             if (leader)
               mma_smem(s_at,
                        q_rows + ((part * Sh::kPartChunks + i / 4) * kTileRows * 128 + i % 4 * 32) / 16,
@@ -459,6 +470,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           }
         }
         if (leader) mma_commit(&s.s_full[t]);
+        if (kTurns && pass) next_turn();
         if (last && leader) mma_commit(&s.q_empty[t]);
       };
       uint32_t q_round = 0, s_round = 0;  // units and steps of this tile
@@ -511,13 +523,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
               __syncwarp();
             }
             if (j == 0 && q_round > 0) ok = wait(&s.o_read[t], (q_round - 1) & 1);
-            if constexpr (kTurns) {
-              ok = ok && wait(&s.p_ready[t][0], s_round & 1) &&
-                   wait(&s.p_ready[t][1], s_round & 1) && (!next || arrived(k_at)) && my_turn();
-            }
+            if constexpr (kTurns) ok = ok && (!next || arrived(k_at));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if constexpr (!kTurns) ok = ok && wait(&s.p_ready[t][h], s_round & 1);
+              ok = ok && wait(&s.p_ready[t][h], s_round & 1);
+              if (kTurns && h == 1) ok = ok && my_turn();
               if (!ok) break;
               tmem_fence_after();
 #pragma unroll
@@ -561,6 +571,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const uint32_t p_at = tmem + lanes + Sh::kP + t * Sh::kPStep;
     const uint32_t o_at = tmem + lanes + Sh::kOut + t * D;
     const float mult = fabsf(p.mult), late = kCapped ? 1.0f : mult;
+    float terms[kTanhTerms];
+#pragma unroll
+    for (int i = 0; i < kTanhTerms; ++i) terms[i] = kTanh[i] * p.cap;
     // how far below the maximum a reference is set, how far above it the maximum
     // may go before it is set anew, and the sum of half a step's P up to which
     // none is too large
@@ -593,16 +606,40 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         uint32_t raw[kKeys];
         float* x = reinterpret_cast<float*>(raw);
         const int base = j * kKeys;
-        auto cap_scores = [&](int h) {
+        const bool edge = base < some_lo || base + kKeys > some_hi;
+        // Capped scores: by a polynomial where all of the warp's |x mult| <= 1 and
+        // nothing is masked, otherwise in place before anything else.
+        bool by_terms = false;
+        // x of a half from what was loaded, masked and ready for the exponentials
+        auto prepare = [&](int h) {
           if constexpr (kCapped) {
+            if (__builtin_expect(!by_terms, 0)) return;
 #pragma unroll
-            for (int e = 64 * h; e < 64 * h + 64; ++e) x[e] = p.cap * kv4::tanh_score(x[e] * mult);
+            for (int e = 64 * h; e < 64 * h + 64; e += 2) {
+              const float2 u = mul2(make_float2(x[e], x[e + 1]), make_float2(mult, mult));
+              const float2 square = mul2(u, u);
+              float2 r = make_float2(terms[kTanhTerms - 1], terms[kTanhTerms - 1]);
+#pragma unroll
+              for (int i = kTanhTerms - 2; i >= 0; --i)
+                r = fma2(r, square, make_float2(terms[i], terms[i]));
+              r = mul2(r, u);
+              x[e] = r.x, x[e + 1] = r.y;
+            }
+          } else if (__builtin_expect(edge, 0)) {
+#pragma unroll
+            for (int c = 64 * h; c < 64 * h + 64; c += 16) {
+              if (base + c + 16 > some_hi) {
+#pragma unroll
+                for (int e = c; e < c + 16; ++e)
+                  if (e >= hi - base) x[e] = -INFINITY;
+              }
+              if (base + c < some_lo) {
+#pragma unroll
+                for (int e = c; e < c + 16; ++e)
+                  if (e < lo - base) x[e] = -INFINITY;
+              }
+            }
           }
-        };
-        auto mask = [&](int h) {
-#pragma unroll
-          for (int e = 64 * h; e < 64 * h + 64; ++e)
-            if (base + e < lo || base + e >= hi) x[e] = -INFINITY;
         };
         auto maximum = [&](int h) {
           float m[4];
@@ -612,7 +649,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           for (int e = 64 * h + 8; e < 64 * h + 64; e += 8)
 #pragma unroll
             for (int f = 0; f < 4; ++f) m[f] = max3(m[f], x[e + f], x[e + f + 4]);
-          return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+          return fmaxf(max3(m[0], m[1], m[2]), m[3]) * late;
         };
         // P of a half, in place, and its sum
         auto exponentials = [&](int h) {
@@ -646,23 +683,45 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         // exponentials.  What most steps do not do stands apart, so that they run
         // straight through their instructions.
         tmem_load128(s_at, raw);
-        cap_scores(0);
-        cap_scores(1);
-        const bool edge = base < some_lo || base + kKeys > some_hi;
-        if (__builtin_expect(edge, 0)) mask(0), mask(1);
+        if constexpr (kCapped) {
+          float most[2] = {0.0f, 0.0f};
+#pragma unroll
+          for (int e = 0; e < kKeys; e += 4) {
+            most[0] = max3(most[0], fabsf(x[e]), fabsf(x[e + 1]));
+            most[1] = max3(most[1], fabsf(x[e + 2]), fabsf(x[e + 3]));
+          }
+          by_terms = !edge && __all_sync(~0u, fmaxf(most[0], most[1]) * mult <= 1.0f);
+          if (__builtin_expect(!by_terms, 0)) {
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 16) {
+              uint32_t part[16];
+              tmem_load16(s_at + c, part);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float y = p.cap * kv4::tanh_score(__uint_as_float(part[e]) * mult);
+                const int at = base + c + e;
+                part[e] = __float_as_uint(at < lo || at >= hi ? -INFINITY : y);
+              }
+              tmem_store16(s_at + c, part);
+            }
+            tmem_wait_store();
+            tmem_load128(s_at, raw);
+          }
+        }
+        prepare(0);
+        prepare(1);
         float sum = 0.0f;
         bool good = false;
         if (__builtin_expect(j > 0, 1)) {
           sum = exponentials(0);
-          good = sum <= kLargest && maximum(1) * late <= ref + kMost && ref > -INFINITY;
+          good = sum <= kLargest && maximum(1) <= ref + kMost && ref > -INFINITY;
         }
         if (__builtin_expect(!__all_sync(~0u, good), 0)) {
           if (j > 0) {
             tmem_load64(s_at, raw);
-            cap_scores(0);
-            if (edge) mask(0);
+            prepare(0);
           }
-          const float top = fmaxf(maximum(0), maximum(1)) * late;
+          const float top = fmaxf(maximum(0), maximum(1));
           float shrink = 1.0f;
           if (!good && top > ref + kBelow) {
             const float next = top - kBelow;
@@ -704,28 +763,42 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       ++o_round;
       tmem_fence_after();
       const float inverse = ok ? (l == 0.0f ? 0.0f : 1.0f / l) : NAN;
-      const int64_t out_row = (int64_t)(u.first + i) * p.q_heads + head;
-      bool finite = true;
+      const int out_row = (u.first + i) * p.q_heads + head;  // rows * q_heads fit
+      const unsigned written = __ballot_sync(~0u, valid);
+      float2 zero[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // NaN once an O is not finite
+      // 64 elements of the warp's rows at a time through shared memory, so that
+      // eight lanes write a row's 128 bytes together (each lane its own row, 16
+      // bytes at a time, took 5000 cycles a unit instead of 1000)
 #pragma unroll
       for (int c = 0; c < D; c += 64) {
         uint32_t o[64];
         tmem_load64(o_at + c, o);
         if (c + 64 == D) arrive(&s.o_read[t]);
 #pragma unroll
-        for (int b = 0; b < 64; b += 8) {
+        for (int b = 0; b < 8; ++b) {
           uint32_t y[4];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float y0 = __uint_as_float(o[b + e]), y1 = __uint_as_float(o[b + e + 1]);
-            finite = finite && fabsf(y0) <= 3.4028234e38f && fabsf(y1) <= 3.4028234e38f;
-            y[e / 2] = round_pair<kHalf>(y0 * inverse, y1 * inverse);
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = make_float2(__uint_as_float(o[8 * b + 2 * e]),
+                                         __uint_as_float(o[8 * b + 2 * e + 1]));
+            zero[e & 1] = fma2(v, make_float2(0.0f, 0.0f), zero[e & 1]);
+            y[e] = round_pair<kHalf>(v.x * inverse, v.y * inverse);
           }
-          if (valid)
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (out_row * D + c + b) * 2) =
-                make_uint4(y[0], y[1], y[2], y[3]);
+          s.rows[warp][lane][b ^ (lane & 7)] = make_uint4(y[0], y[1], y[2], y[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int r = lane >> 3; r < 32; r += 4) {
+          const int to = __shfl_sync(~0u, out_row, r);
+          if (written >> r & 1)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + ((int64_t)to * D + c) * 2 +
+                                      (lane & 7) * 16) = s.rows[warp][r][(lane ^ r) & 7];
+        }
+        __syncwarp();
       }
       if (valid) p.lse[out_row] = !ok ? NAN : l == 0.0f ? -INFINITY : kLn2 * (ref + log2f(l));
+      const float2 none = add2(zero[0], zero[1]);
+      const bool finite = none.x + none.y == 0.0f;
       // a NaN among the scores that the row sees makes the sum NaN, and is right
       unsigned again = __ballot_sync(~0u, ok && valid && !finite && l == l);
       while (again) {

@@ -112,6 +112,7 @@ struct Finder {
   int level = -1;            // the block whose units are being taken
   int behind = 0, here = 0;  // units of later blocks, and of this one
   int base = 0, passed = 0;  // this block's units in the sequences before base
+  int total = -1;            // units, once known
 
   __device__ int blocks(const Params& p, int tokens, int b) const {
     if (b >= p.num_seqs) return 0;
@@ -121,25 +122,27 @@ struct Finder {
   // units whose block is `from` or later
   __device__ int count(const Params& p, int tokens, int from) const {
     int c = 0;
+#pragma unroll 1
     for (int b = threadIdx.x & 31; b < p.num_seqs; b += 32)
       c += max(0, blocks(p, tokens, b) - from);
     return __reduce_add_sync(~0u, c);
   }
 
-  __device__ Unit find(const Params& p, int tokens, int u) {
+  __device__ __forceinline__ Unit find(const Params& p, int tokens, int u) {
     const int lane = threadIdx.x & 31;
     if (u < behind + passed) *this = Finder();
+    if (total < 0) total = count(p, tokens, 0);
+    if (u >= total) return Unit{0, 0, -1, 0};
     if (level < 0 || u >= behind + here) {
-      int lo = 0, hi = level, at_hi = behind, at_lo;
+      int lo = 0, hi = level, at_hi = behind, at_lo = total;
       if (level < 0) {
         hi = 0;
+#pragma unroll 1
         for (int b = lane; b < p.num_seqs; b += 32) hi = max(hi, blocks(p, tokens, b));
         hi = __reduce_max_sync(~0u, hi);
       } else {
         at_hi += here;
       }
-      at_lo = count(p, tokens, 0);
-      if (u >= at_lo) return Unit{0, 0, -1, 0};
       while (hi - lo > 1) {  // the last block with more than u units from it on
         const int mid = (lo + hi) >> 1;
         const int c = count(p, tokens, mid);
@@ -148,6 +151,7 @@ struct Finder {
       level = lo, behind = at_hi, here = at_lo - at_hi;
       base = passed = 0;
     }
+#pragma unroll 1
     for (; base < p.num_seqs; base += 32) {
       const unsigned has = __ballot_sync(~0u, blocks(p, tokens, base + lane) > level);
       const int left = u - behind - passed;
@@ -251,12 +255,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   kv4::grid_dependency_wait();
 
-  Finder finder;
-  if (warp == Sh::kRowWarps + 2) {
-    Unit u = finder.find(p, kTiles * a.tokens, blockIdx.x / a.sets);
-    u.set = blockIdx.x % a.sets;
-    if (lane == 0) s.unit[0] = u;
-  }
   if (warp == Sh::kRowWarps) {
     if (lane == 0) {
       mbar_init(&s.fetch_done, 1);
@@ -282,8 +280,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
     __syncwarp();
   }
-  __syncthreads();
-  if (s.unit[0].q0 < 0) return;  // the grid has a CTA for as many units as there can be
   if (warp == Sh::kRowWarps) tmem_allocate(&s.tmem, Sh::kColumns);
   tmem_fence_before();
   __syncthreads();
@@ -311,16 +307,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kOtherRegisters));
     if (warp == Sh::kRowWarps + 2) {
       // --------------------------------------------------------------- units
-      if (lane == 0) mbar_arrive(&s.unit_full[0]);
-      // No more are taken than the SMs cannot begin at once.
-      bool more = gridDim.x > (unsigned)a.sms;
-      for (int k = 1;; ++k) {
+      // This CTA's, then those of CTAs that have not started.  No more are taken
+      // than the SMs cannot begin at once; what the grid has beyond the last unit
+      // is taken too and needs no CTA.
+      Finder finder;
+      uint32_t index = blockIdx.x;
+      bool here = true, more = gridDim.x > (unsigned)a.sms;
+      int fetches = 0;
+#pragma unroll 1
+      for (int k = 0;;) {
         // whether the CTA has given up or not: what was taken has to be handed on
         if (k >= kRing &&
             !mbar_wait_bounded(&s.unit_empty[k % kRing], (k / kRing - 1) & 1, 2 * kPatience))
           break;
-        Unit u{0, 0, -1, 0};
-        if (more && !s.given_up) {
+        if (!here && more && !s.given_up) {
           uint32_t taken = 0, x = 0;
           if (lane == 0) {
             async_proxy_fence();
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 : "memory");
           }
           __syncwarp();
-          if (wait(&s.fetch_done, (k - 1) & 1)) {
+          if (wait(&s.fetch_done, fetches++ & 1)) {
             asm volatile(
                 "{\n .reg .pred p;\n .reg .b128 h;\n ld.shared.b128 h, [%2];\n"
                 " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
@@ -342,11 +342,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 : "r"(smem_u32(&s.fetched))
                 : "memory");
           }
-          more = taken != 0;
-          if (taken) {
-            u = finder.find(p, kTiles * a.tokens, x / a.sets);
-            u.set = x % a.sets;
-          }
+          here = more = taken != 0;
+          index = x;
+        }
+        Unit u{0, 0, -1, 0};
+        if (here) {
+          u = finder.find(p, kTiles * a.tokens, index / a.sets);
+          u.set = index % a.sets;
+          here = false;
+          if (u.q0 < 0 && more) continue;
         }
         if (lane == 0) {
           s.unit[k % kRing] = u;
@@ -354,6 +358,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         }
         __syncwarp();
         if (u.q0 < 0) break;
+        ++k;
       }
     } else if (warp == Sh::kRowWarps + 1) {
       // -------------------------------------------------------------- copies
@@ -376,6 +381,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             tensor_load_3d(s.q[t] + c * kTileRows * 128, &q_map, c * 64, w.head0,
                            u.first + u.q0 + t * a.tokens, &s.q_full[t]);
         }
+#pragma unroll 1
         for (int i = 0; ok && i < 2 * w.most * kParts; ++i) {
           const int slot = at % kStages, round = at / kStages;
           ok = round == 0 || wait_for(&s.empty[slot], (round - 1) & 1, &s.given_up, a.status);
@@ -607,40 +613,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         float* x = reinterpret_cast<float*>(raw);
         const int base = j * kKeys;
         const bool edge = base < some_lo || base + kKeys > some_hi;
-        // Capped scores: by a polynomial where all of the warp's |x mult| <= 1 and
-        // nothing is masked, otherwise in place before anything else.
-        bool by_terms = false;
-        // x of a half from what was loaded, masked and ready for the exponentials
-        auto prepare = [&](int h) {
-          if constexpr (kCapped) {
-            if (__builtin_expect(!by_terms, 0)) return;
-#pragma unroll
-            for (int e = 64 * h; e < 64 * h + 64; e += 2) {
-              const float2 u = mul2(make_float2(x[e], x[e + 1]), make_float2(mult, mult));
-              const float2 square = mul2(u, u);
-              float2 r = make_float2(terms[kTanhTerms - 1], terms[kTanhTerms - 1]);
-#pragma unroll
-              for (int i = kTanhTerms - 2; i >= 0; --i)
-                r = fma2(r, square, make_float2(terms[i], terms[i]));
-              r = mul2(r, u);
-              x[e] = r.x, x[e + 1] = r.y;
-            }
-          } else if (__builtin_expect(edge, 0)) {
-#pragma unroll
-            for (int c = 64 * h; c < 64 * h + 64; c += 16) {
-              if (base + c + 16 > some_hi) {
-#pragma unroll
-                for (int e = c; e < c + 16; ++e)
-                  if (e >= hi - base) x[e] = -INFINITY;
-              }
-              if (base + c < some_lo) {
-#pragma unroll
-                for (int e = c; e < c + 16; ++e)
-                  if (e < lo - base) x[e] = -INFINITY;
-              }
-            }
-          }
-        };
         auto maximum = [&](int h) {
           float m[4];
 #pragma unroll
@@ -682,34 +654,58 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         // it was good, as does the second half's maximum, which is found beside the
         // exponentials.  What most steps do not do stands apart, so that they run
         // straight through their instructions.
-        tmem_load128(s_at, raw);
-        if constexpr (kCapped) {
-          float most[2] = {0.0f, 0.0f};
-#pragma unroll
-          for (int e = 0; e < kKeys; e += 4) {
-            most[0] = max3(most[0], fabsf(x[e]), fabsf(x[e + 1]));
-            most[1] = max3(most[1], fabsf(x[e + 2]), fabsf(x[e + 3]));
-          }
-          by_terms = !edge && __all_sync(~0u, fmaxf(most[0], most[1]) * mult <= 1.0f);
-          if (__builtin_expect(!by_terms, 0)) {
+        // Caps and masks: in tensor memory, in a loop.  (Unrolled over the registers
+        // they were so much code that instructions came from the second-level
+        // cache: with caps 1977 us instead of 577, without 419 instead of 317, for 33
+        // prompts of 2048 rows with a window of 1000.)
+        if (kCapped || __builtin_expect(edge, 0)) {
+          constexpr int kPiece = kCapped ? 32 : 16;
 #pragma unroll 1
-            for (int c = 0; c < kKeys; c += 16) {
-              uint32_t part[16];
-              tmem_load16(s_at + c, part);
+          for (int c = 0; c < kKeys; c += kPiece) {
+            const bool inside = base + c + kPiece <= some_hi && base + c >= some_lo;
+            if (!kCapped && inside) continue;
+            uint32_t piece[kPiece];
+            float* y = reinterpret_cast<float*>(piece);
+            if constexpr (kCapped) tmem_load32(s_at + c, piece);
+            else tmem_load16(s_at + c, piece);
+            const int from = lo - base - c, to = hi - base - c;  // what the row sees of them
+            if constexpr (kCapped) {
+              if (!inside) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float y = p.cap * kv4::tanh_score(__uint_as_float(part[e]) * mult);
-                const int at = base + c + e;
-                part[e] = __float_as_uint(at < lo || at >= hi ? -INFINITY : y);
+                for (int e = 0; e < kPiece; ++e)
+                  if (e < from || e >= to) y[e] = 0.0f;
               }
-              tmem_store16(s_at + c, part);
+              float most = 0.0f;
+#pragma unroll
+              for (int e = 0; e < kPiece; e += 2) most = max3(most, fabsf(y[e]), fabsf(y[e + 1]));
+              if (__all_sync(~0u, most * mult <= 1.0f)) {
+#pragma unroll
+                for (int e = 0; e < kPiece; e += 2) {
+                  const float2 u = mul2(make_float2(y[e], y[e + 1]), make_float2(mult, mult));
+                  const float2 square = mul2(u, u);
+                  float2 r = make_float2(terms[kTanhTerms - 1], terms[kTanhTerms - 1]);
+#pragma unroll
+                  for (int i = kTanhTerms - 2; i >= 0; --i)
+                    r = fma2(r, square, make_float2(terms[i], terms[i]));
+                  r = mul2(r, u);
+                  y[e] = r.x, y[e + 1] = r.y;
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < kPiece; ++e) y[e] = p.cap * kv4::tanh_score(y[e] * mult);
+              }
             }
-            tmem_wait_store();
-            tmem_load128(s_at, raw);
+            if (!inside) {
+#pragma unroll
+              for (int e = 0; e < kPiece; ++e)
+                if (e < from || e >= to) y[e] = -INFINITY;
+            }
+            if constexpr (kCapped) tmem_store32(s_at + c, piece);
+            else tmem_store16(s_at + c, piece);
           }
+          tmem_wait_store();
         }
-        prepare(0);
-        prepare(1);
+        tmem_load128(s_at, raw);
         float sum = 0.0f;
         bool good = false;
         if (__builtin_expect(j > 0, 1)) {
@@ -719,7 +715,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         if (__builtin_expect(!__all_sync(~0u, good), 0)) {
           if (j > 0) {
             tmem_load64(s_at, raw);
-            prepare(0);
           }
           const float top = fmaxf(maximum(0), maximum(1));
           float shrink = 1.0f;
@@ -768,8 +763,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       float2 zero[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // NaN once an O is not finite
       // 64 elements of the warp's rows at a time through shared memory, so that
       // eight lanes write a row's 128 bytes together (each lane its own row, 16
-      // bytes at a time, took 5000 cycles a unit instead of 1000)
-#pragma unroll
+      // bytes at a time, took 5000 cycles a unit instead of 2500)
+#pragma unroll 1
       for (int c = 0; c < D; c += 64) {
         uint32_t o[64];
         tmem_load64(o_at + c, o);

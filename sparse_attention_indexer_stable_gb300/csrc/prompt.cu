@@ -111,13 +111,18 @@ static dcp_status launch_tiles(const dcp_prompt_attention_args* a, TileParams p,
   p.tokens = kTileRows / p.packed;
   p.sets = a->q_heads / p.packed;
   p.q_bytes = S::kChunks * p.packed * p.tokens * 128;
-  CUtensorMap q, k, v;
+  // 32 rows of a tile: whole tokens of its heads, or heads of one token
+  p.out_box = 32 % p.packed == 0 || p.packed % 32 == 0;
+  const int out_heads = p.packed < 32 ? p.packed : 32;
+  CUtensorMap q, k, v, out;
   if (!map_of(&q, a->q, a->dtype, a->rows, a->q_row_stride, a->q_heads, a->q_head_stride, D,
               p.packed, p.tokens) ||
       !map_of(&k, a->k, a->dtype, a->rows, a->k_row_stride, a->kv_heads, a->k_head_stride, D, 1,
               kKeys) ||
       !map_of(&v, a->v, a->dtype, a->rows, a->v_row_stride, a->kv_heads, a->v_head_stride, D, 1,
-              kKeys))
+              kKeys) ||
+      !map_of(&out, a->out, a->dtype, a->rows, (int64_t)a->q_heads * D, a->q_heads, D, D,
+              p.out_box ? out_heads : 1, p.out_box ? 32 / out_heads : 1))
     return DCP_ERR_CUDA;
   // as many units as there can be, whatever the lengths
   const int64_t by_span = a->rows / (S::kTiles * p.tokens) + a->num_seqs;
@@ -126,7 +131,7 @@ static dcp_status launch_tiles(const dcp_prompt_attention_args* a, TileParams p,
   auto* kernel = half ? (p.p.capped ? tiles_kernel<D, true, true> : tiles_kernel<D, true, false>)
                       : (p.p.capped ? tiles_kernel<D, false, true> : tiles_kernel<D, false, false>);
   return status_of(kv4::launch(kernel, dim3((unsigned)(units * p.sets)), S::kThreads,
-                               sizeof(Shared<D>) + 1024, 1, stream, p, q, k, v));
+                               sizeof(Shared<D>) + 1024, 1, stream, p, q, k, v, out));
 }
 
 extern "C" dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* a,

@@ -102,6 +102,7 @@ struct TileParams {
   int sets;    // of packed heads: kv_heads * group / packed
   int sms;
   uint32_t q_bytes;  // of a tile's copy
+  int out_box;       // whether 32 of a tile's rows are a box of the output
 };
 
 // Finds the u-th unit of the sequences (quickly where u grows from call to call);
@@ -246,7 +247,8 @@ template <int D, bool kHalf, bool kCapped>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     tiles_kernel(const TileParams a, const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap k_map,
-                 const __grid_constant__ CUtensorMap v_map) {
+                 const __grid_constant__ CUtensorMap v_map,
+                 const __grid_constant__ CUtensorMap out_map) {
   using Sh = Shape<D>;
   constexpr int kTiles = Sh::kTiles, kStages = Sh::kStages, kParts = Sh::kParts;
   extern __shared__ uint8_t tiles_smem[];
@@ -591,7 +593,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       if (lane == 0) mbar_arrive(bar);
     };
     int s_round = 0, o_round = 0;  // phases of s_full and o_done
-    bool ok = true;
+    // Waits that have given up end at once: the rest of the unit is computed on
+    // whatever there is, and becomes NaN.
+    auto wait_here = [&](unsigned long long* bar, uint32_t parity) {
+      wait_for(bar, parity, &s.given_up, a.status);
+      __syncwarp();
+      tmem_fence_after();
+    };
     Unit u;
     for (int k = 0; unit_at(k, &u); unit_done(k++)) {
       const Walk<D> w(a, u);
@@ -603,12 +611,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       const int lo = valid && p.window ? max(0, i - p.window + 1) - w.from : 0;
       const int hi = valid ? (p.causal ? i + 1 : u.n) - w.from : INT32_MAX;
       const int some_lo = __reduce_max_sync(~0u, lo), some_hi = __reduce_min_sync(~0u, hi);
+      const int least_lo = __reduce_min_sync(~0u, valid ? lo : INT32_MAX);
+      const int most_hi = __reduce_max_sync(~0u, valid ? hi : 0);
       float ref = -INFINITY, l = 0.0f, over = 0.0f;  // over: what l is too large by
-      for (int j = 0; ok && j < steps; ++j) {
-        ok = wait(&s.s_full[t], s_round & 1);
-        if (!ok) break;
-        ++s_round;
-        tmem_fence_after();
+      for (int j = 0; j < steps; ++j) {
+        wait_here(&s.s_full[t], s_round++ & 1);
         uint32_t raw[kKeys];
         float* x = reinterpret_cast<float*>(raw);
         const int base = j * kKeys;
@@ -643,10 +650,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         // P over S: this step's S came after it.
         bool last_done = !Sh::kBeside || j == 0;
         auto wait_last = [&] {
-          if (!last_done) {
-            ok = wait(&s.o_done[t], o_round++ & 1);
-            tmem_fence_after();
-          }
+          if (!last_done) wait_here(&s.o_done[t], o_round++ & 1);
           last_done = true;
         };
         // Most steps leave the reference where it is.  So the first half is
@@ -666,6 +670,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (!kCapped && inside) continue;
             uint32_t piece[kPiece];
             float* y = reinterpret_cast<float*>(piece);
+            if (base + c >= most_hi || base + c + kPiece <= least_lo) {
+#pragma unroll
+              for (int e = 0; e < kPiece; ++e) y[e] = -INFINITY;
+              if constexpr (kCapped) tmem_store32(s_at + c, piece);
+              else tmem_store16(s_at + c, piece);
+              continue;
+            }
             if constexpr (kCapped) tmem_load32(s_at + c, piece);
             else tmem_load16(s_at + c, piece);
             const int from = lo - base - c, to = hi - base - c;  // what the row sees of them
@@ -727,7 +738,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           }
           if (j > 0) {
             wait_last();
-            if (!ok) break;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -742,7 +752,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         }
         if constexpr (Sh::kBeside) arrive(&s.s_read[t]);
         wait_last();
-        if (!ok) break;
         tmem_store32(p_at, raw);
         tmem_wait_store();
         arrive(&s.p_ready[t][0]);
@@ -754,21 +763,24 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         over = (now - l) - add;
         l = now;
       }
-      ok = ok && wait(&s.o_done[t], o_round & 1);
-      ++o_round;
-      tmem_fence_after();
+      wait_here(&s.o_done[t], o_round++ & 1);
+      const bool ok = !*(volatile int*)&s.given_up;
       const float inverse = ok ? (l == 0.0f ? 0.0f : 1.0f / l) : NAN;
       const int out_row = (u.first + i) * p.q_heads + head;  // rows * q_heads fit
       const unsigned written = __ballot_sync(~0u, valid);
       float2 zero[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // NaN once an O is not finite
-      // 64 elements of the warp's rows at a time through shared memory, so that
-      // eight lanes write a row's 128 bytes together (each lane its own row, 16
-      // bytes at a time, took 5000 cycles a unit instead of 2500)
+      // 64 elements of the warp's rows at a time through shared memory: from there
+      // by a tensor copy where the rows make a box and all are there, otherwise
+      // eight lanes write a row's 128 bytes together.  (Each lane its own row, 16
+      // bytes at a time, took 5000 cycles a unit; the copies are not waited for.)
+      const bool box = a.out_box && written == ~0u;
 #pragma unroll 1
       for (int c = 0; c < D; c += 64) {
         uint32_t o[64];
         tmem_load64(o_at + c, o);
         if (c + 64 == D) arrive(&s.o_read[t]);
+        if (lane == 0) bulk_wait_read();  // what was copied from here before
+        __syncwarp();
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
           uint32_t y[4];
@@ -780,6 +792,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             y[e] = round_pair<kHalf>(v.x * inverse, v.y * inverse);
           }
           s.rows[warp][lane][b ^ (lane & 7)] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        if (box) {
+          async_proxy_fence();
+          __syncwarp();
+          if (lane == 0) {
+            const int first_row = 32 * (warp & 3), in_tile = first_row / a.packed;
+            tensor_store_3d(&out_map, s.rows[warp], c, w.head0 + first_row - in_tile * a.packed,
+                            u.first + u.q0 + t * a.tokens + in_tile);
+            bulk_commit();
+          }
+          continue;
         }
         __syncwarp();
 #pragma unroll
@@ -796,6 +819,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       const bool finite = none.x + none.y == 0.0f;
       // a NaN among the scores that the row sees makes the sum NaN, and is right
       unsigned again = __ballot_sync(~0u, ok && valid && !finite && l == l);
+      if (again) {
+        if (lane == 0) bulk_wait();  // those rows are written once more
+        __syncwarp();
+      }
       while (again) {
         const int r = __ffs(again) - 1;
         again &= again - 1;
@@ -803,6 +830,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       }
     }
   }
+  if (warp < Sh::kRowWarps && lane == 0) bulk_wait_read();
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();

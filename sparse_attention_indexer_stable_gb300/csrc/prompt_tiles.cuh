@@ -383,18 +383,25 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             tensor_load_3d(s.q[t] + c * kTileRows * 128, &q_map, c * 64, w.head0,
                            u.first + u.q0 + t * a.tokens, &s.q_full[t]);
         }
+        // In the order of use: K0 V0 K1 V1 ..., or, with P beside S, K0 K1 V0 K2 V1
+        // ...: a stage is filled again only when all before it in this order are
+        // (heads of 256, four stages: 325 us in the first order, QQ in the second).
 #pragma unroll 1
-        for (int i = 0; ok && i < 2 * w.most * kParts; ++i) {
-          const int slot = at % kStages, round = at / kStages;
-          ok = round == 0 || wait_for(&s.empty[slot], (round - 1) & 1, &s.given_up, a.status);
-          if (!ok) break;
-          ++at;
-          const int step = i / (2 * kParts), part = i % kParts;
-          mbar_expect_tx(&s.full[slot], Sh::kStageBytes);
-          for (int c = 0; c < Sh::kPartChunks; ++c)
-            tensor_load_3d(s.stage[slot] + c * kKeys * 128,
-                           i / kParts % 2 ? &v_map : &k_map, (part * Sh::kPartChunks + c) * 64,
-                           w.kv, u.first + w.from + step * kKeys, &s.full[slot]);
+        for (int i = 0; ok && i < 2 * w.most; ++i) {
+          const bool value = Sh::kBeside ? i == 2 * w.most - 1 || (i > 0 && i % 2 == 0) : i % 2;
+          const int step = !Sh::kBeside || i == 0 ? i / 2 : value ? (i - 1) / 2 : (i + 1) / 2;
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+            const int slot = at % kStages, round = at / kStages;
+            ok = round == 0 || wait_for(&s.empty[slot], (round - 1) & 1, &s.given_up, a.status);
+            if (!ok) break;
+            ++at;
+            mbar_expect_tx(&s.full[slot], Sh::kStageBytes);
+            for (int c = 0; c < Sh::kPartChunks; ++c)
+              tensor_load_3d(s.stage[slot] + c * kKeys * 128, value ? &v_map : &k_map,
+                             (part * Sh::kPartChunks + c) * 64, w.kv,
+                             u.first + w.from + step * kKeys, &s.full[slot]);
+          }
         }
       }
       if (lane == 0 && s.given_up) {  // copies in flight, each for a limited time
@@ -502,10 +509,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         if (!ok) continue;
         free(first_k);
         for (int j = 0; ok && j < w.most; ++j) {
-          const Stages v_at = take();
-          Stages k_at{};
           const bool next = j + 1 < w.most;
-          if (next) k_at = take();
+          Stages v_at, k_at{};
+          if (Sh::kBeside && next) k_at = take();
+          v_at = take();
+          if (!Sh::kBeside && next) k_at = take();
           auto next_scores = [&] {
             if (!kTurns || j >= steps) ok = arrived(k_at);
             if (j + 1 < steps) {
@@ -515,7 +523,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
               next_turn();
             }
           };
-          if (Sh::kBeside && next) next_scores();
+          if (Sh::kBeside && next) {
+            next_scores();
+            if (ok) free(k_at);
+          }
           ok = ok && arrived(v_at);
           if (!ok) break;
           if (j < steps) {
@@ -558,7 +569,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           if (!Sh::kBeside && next) next_scores();
           if (kTurns && !next) next_turn();
           free(v_at);
-          if (next) free(k_at);
+          if (!Sh::kBeside && next) free(k_at);
         }
         q_round += steps > 0;
       }

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         }
         // In the order of use: K0 V0 K1 V1 ..., or, with P beside S, K0 K1 V0 K2 V1
         // ...: a stage is filled again only when all before it in this order are
-        // (heads of 256, four stages: 325 us in the first order, QQ in the second).
+        // (heads of 256, four stages: 325 us in the first order, 210 in the second).
 #pragma unroll 1
         for (int i = 0; ok && i < 2 * w.most; ++i) {
           const bool value = Sh::kBeside ? i == 2 * w.most - 1 || (i > 0 && i % 2 == 0) : i % 2;
@@ -449,16 +449,21 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         }
         return g;
       };
+      auto part_arrived = [&](const Stages& g, int i) {
+        return wait(&s.full[g.slot[i]], g.phase[i]);
+      };
+      auto free_part = [&](const Stages& g, int i) {
+        if (leader) mma_commit(&s.empty[g.slot[i]]);
+      };
       auto arrived = [&](const Stages& g) {
         bool ok = true;
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) ok = ok && wait(&s.full[g.slot[i]], g.phase[i]);
+        for (int i = 0; i < kParts; ++i) ok = ok && part_arrived(g, i);
         return ok;
       };
       auto free = [&](const Stages& g) {
 #pragma unroll
-        for (int i = 0; i < kParts; ++i)
-          if (leader) mma_commit(&s.empty[g.slot[i]]);
+        for (int i = 0; i < kParts; ++i) free_part(g, i);
       };
       // P over S: the tiles' products take turns, so that each tile's next S comes
       // soon (mixed they took 3700 cycles a step of both tiles).  A turn begins
@@ -470,11 +475,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         if (leader) mbar_arrive(&s.turn[kTiles - 1 - t]);
         ++turns;
       };
-      // S from g; `last`: of the unit
-      auto multiply_scores = [&](const Stages& g, bool last, bool pass) {
-        tmem_fence_after();
+      // S from g, which it frees; `first`, `last`: of the unit
+      auto multiply_scores = [&](const Stages& g, bool first, bool last) {
+        bool ok = true;
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
+          if (!kTurns || first) ok = ok && part_arrived(g, part);  // else seen before the turn
+          if (!ok) return false;
+          tmem_fence_after();
           const uint64_t rows = k_rows + g.slot[part] * kStageStep;
 #pragma unroll
           for (int i = 0; i < Sh::kPart / 16; ++i) {
@@ -483,10 +491,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                        q_rows + ((part * Sh::kPartChunks + i / 4) * kTileRows * 128 + i % 4 * 32) / 16,
                        rows + (i / 4 * kKeys * 128 + i % 4 * 32) / 16, scores, part > 0 || i > 0);
           }
+          if (part + 1 < kParts) free_part(g, part);
         }
         if (leader) mma_commit(&s.s_full[t]);
-        if (kTurns && pass) next_turn();
+        if (kTurns && !first) next_turn();
+        free_part(g, kParts - 1);
         if (last && leader) mma_commit(&s.q_empty[t]);
+        return true;
       };
       uint32_t q_round = 0, s_round = 0;  // units and steps of this tile
       bool ok = true;
@@ -500,14 +511,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         // the first step's scores, then each step's next ones and its products
         // with the values; stages that only the other tile needs are passed on
         const Stages first_k = take();
-        ok = arrived(first_k);
         if (steps > 0) {
-          ok = ok && wait(&s.q_full[t], q_round & 1) &&
-               (!Sh::kBeside || s_round == 0 || wait(&s.s_read[t], (s_round - 1) & 1));
-          if (ok) multiply_scores(first_k, steps == 1, false);
+          ok = wait(&s.q_full[t], q_round & 1) &&
+               (!Sh::kBeside || s_round == 0 || wait(&s.s_read[t], (s_round - 1) & 1)) &&
+               multiply_scores(first_k, true, steps == 1);
+        } else {
+          ok = arrived(first_k);
+          if (ok) free(first_k);
         }
-        if (!ok) continue;
-        free(first_k);
         for (int j = 0; ok && j < w.most; ++j) {
           const bool next = j + 1 < w.most;
           Stages v_at, k_at{};
@@ -515,18 +526,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           v_at = take();
           if (!Sh::kBeside && next) k_at = take();
           auto next_scores = [&] {
-            if (!kTurns || j >= steps) ok = arrived(k_at);
             if (j + 1 < steps) {
-              if (Sh::kBeside) ok = ok && wait(&s.s_read[t], s_round & 1);
-              if (ok) multiply_scores(k_at, j + 2 == steps, true);
-            } else if constexpr (kTurns) {
-              next_turn();
+              if (Sh::kBeside) ok = wait(&s.s_read[t], s_round & 1);
+              ok = ok && multiply_scores(k_at, false, j + 2 == steps);
+            } else {
+              ok = arrived(k_at);
+              if (ok) free(k_at);
+              if constexpr (kTurns) next_turn();
             }
           };
-          if (Sh::kBeside && next) {
-            next_scores();
-            if (ok) free(k_at);
-          }
+          if (Sh::kBeside && next) next_scores();
           ok = ok && arrived(v_at);
           if (!ok) break;
           if (j < steps) {
@@ -557,6 +566,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                   if (leader)
                     mma_tmem(o_at + part * Sh::kPart, p_at + i * 8, rows + i * 2048 / 16, kOuts,
                              i > 0 || j > 0);
+                if (kParts > 1 && h == 1) free_part(v_at, part);
               }
             }
             if (!ok) break;
@@ -568,8 +578,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           if (!ok) break;
           if (!Sh::kBeside && next) next_scores();
           if (kTurns && !next) next_turn();
-          free(v_at);
-          if (!Sh::kBeside && next) free(k_at);
+          if (kParts == 1 || j >= steps) free(v_at);
         }
         q_round += steps > 0;
       }

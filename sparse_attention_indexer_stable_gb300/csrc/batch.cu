@@ -35,6 +35,11 @@ cudaError_t allow_extend() {
   return e;
 }
 
+// Whether n numbers at a and m at b share memory.
+bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  return n > 0 && m > 0 && (uintptr_t)a < (uintptr_t)(b + m) && (uintptr_t)b < (uintptr_t)(a + n);
+}
+
 // Whether 16-byte pieces fit a plane of heads: its address and its strides.
 bool fits(const void* p, int64_t row, int64_t head, int64_t per) {
   return ((uintptr_t)p & 15) == 0 && row % per == 0 && head % per == 0;
@@ -90,12 +95,16 @@ dcp_status dcp_kv4_extend(const dcp_kv4_extend_args* a, dcp_stream_t stream) {
   p.table_width = a->table_width;
   p.num_free = a->num_free;
   p.places = a->places;
+  const bool in_place = overlap(a->out_lens, a->num_seqs, a->lens, a->num_seqs) ||
+                        overlap(a->out_lens, a->num_seqs, a->used, 1) ||
+                        overlap(a->out_used, 1, a->lens, a->num_seqs) ||
+                        overlap(a->out_used, 1, a->used, 1);
   int ctas = 1;
-  while (ctas < 8 && (int64_t)ctas * kv4::kExtendThreads < a->places) ctas *= 2;
+  while (ctas < (in_place ? 8 : 64) && (int64_t)ctas * kv4::kExtendThreads < a->places) ctas *= 2;
   if (allow_extend() != cudaSuccess) return DCP_ERR_CUDA;
   return status_of(kv4::launch(kv4::extend_kernel, dim3((unsigned)ctas), kv4::kExtendThreads,
-                               (size_t)a->num_seqs * kv4::kExtendRow, ctas, (cudaStream_t)stream,
-                               p));
+                               (size_t)a->num_seqs * kv4::kExtendRow, in_place ? ctas : 1,
+                               (cudaStream_t)stream, p));
 }
 
 dcp_status dcp_rotary(const dcp_rotary_args* a, dcp_stream_t stream) {
@@ -134,8 +143,19 @@ dcp_status dcp_rotary(const dcp_rotary_args* a, dcp_stream_t stream) {
   const int v = vec ? per : 1;
   p.turn_items = p.pairs / v;
   p.items = p.turn_items + (a->dim - a->turned) / v;
-  p.tokens_per_cta = 1;
+  // Tokens together until a CTA has 1024 items, unless that leaves SMs without
+  // work.  (Items of a CTA stay below the 2^16 that divide() is exact for: more
+  // heads than that take the grid's second dimension.)
   p.heads_per_cta = p.heads;
+  while ((int64_t)p.heads_per_cta * p.items > 32768) p.heads_per_cta = (p.heads_per_cta + 1) / 2;
+  p.per_token = p.heads_per_cta * p.items;
+  p.tokens_per_cta = 1;
+  while (p.tokens_per_cta < 8 && p.tokens_per_cta * p.per_token < 1024 &&
+         a->tokens > (int64_t)p.tokens_per_cta * 8 * 152)
+    p.tokens_per_cta *= 2;
+  p.by_token = division_by((uint32_t)p.per_token);
+  p.by_head = division_by((uint32_t)p.items);
+  p.by_pairs = division_by((uint32_t)p.pairs);
   const dim3 grid((unsigned)((a->tokens + p.tokens_per_cta - 1) / p.tokens_per_cta),
                   (unsigned)((p.heads + p.heads_per_cta - 1) / p.heads_per_cta));
   const bool il = a->interleaved != 0;

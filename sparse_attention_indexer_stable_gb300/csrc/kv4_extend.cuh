@@ -7,11 +7,11 @@
 // free[first_b + p / P - pages(l_b)] otherwise; the token that opens a page
 // also writes it into the table.
 //
-// One cluster of up to 8 CTAs in one launch: each CTA sums over all sequences
-// (a few numbers per thread), so that nothing has to be passed between CTAs,
-// and takes its stripe of the places.  The cluster's barrier stands between the
-// last read of lens and used and their new values, which may go to the same
-// memory.
+// One launch: each CTA sums over all sequences (a few numbers per thread), so that
+// nothing has to be passed between CTAs, and takes its stripe of the places.  Where
+// the new lens or used go to the memory of the old ones, the CTAs are one cluster
+// of up to 8, whose barrier stands between the last read and the first write.
+// Latency bounds it: 256 places 3.9 us, 65536 4.2 (in one cluster 10.3).
 #pragma once
 
 #include "kv4_common.cuh"
@@ -37,16 +37,6 @@ __device__ __forceinline__ int clamp_int(int64_t x) {
   return x > INT32_MAX ? INT32_MAX : (int)x;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t n;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -110,7 +100,7 @@ __global__ void __launch_bounds__(kExtendThreads, 1) extend_kernel(const ExtendP
     }
   }
   const int total = (int)min(tokens, (int64_t)p.places);
-  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  const uint32_t rank = blockIdx.x, ctas = gridDim.x;  // of a cluster, or with no barrier between
   cluster_arrive();  // this CTA has read its lens and used
   __syncthreads();
 

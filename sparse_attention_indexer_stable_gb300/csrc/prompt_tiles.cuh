@@ -554,7 +554,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if constexpr (kTurns) ok = ok && (!next || arrived(k_at));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              ok = ok && wait(&s.p_ready[t][h], s_round & 1);
+              if (!Sh::kBeside || h == 0)
+                ok = ok && wait(&s.p_ready[t][Sh::kBeside ? 1 : h], s_round & 1);
               if (kTurns && h == 1) ok = ok && my_turn();
               if (!ok) break;
               tmem_fence_after();
@@ -770,13 +771,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           }
           sum = exponentials(0);
         }
-        if constexpr (Sh::kBeside) arrive(&s.s_read[t]);
-        wait_last();
-        tmem_store32(p_at, raw);
-        tmem_wait_store();
-        arrive(&s.p_ready[t][0]);
-        sum += exponentials(1);
-        tmem_store32(p_at + 32, raw + 64);
+        if constexpr (Sh::kBeside) {
+          // the rows, not the products, are what a step waits for: P at once
+          arrive(&s.s_read[t]);
+          sum += exponentials(1);
+          wait_last();
+          tmem_store32(p_at, raw);
+          tmem_store32(p_at + 32, raw + 64);
+        } else {
+          tmem_store32(p_at, raw);
+          tmem_wait_store();
+          arrive(&s.p_ready[t][0]);
+          sum += exponentials(1);
+          tmem_store32(p_at + 32, raw + 64);
+        }
         tmem_wait_store();
         arrive(&s.p_ready[t][1]);
         const float add = sum - over, now = l + add;

@@ -28,6 +28,9 @@ static unsigned int* g_status[64];  // each device's status word, before g_ready
 static int g_sms[64];               // and its SMs
 static EncodeTiled g_encode;        // likewise
 static std::mutex g_mutex;
+#ifdef DCP_DEBUG_POISON
+static std::atomic<int> g_withheld[3] = {{-1}, {-1}, {-1}};  // see dcp_prompt_selftest_withhold
+#endif
 
 template <int D, bool kHalf>
 static cudaError_t allow_tiles() {
@@ -173,9 +176,21 @@ extern "C" dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* a,
   // finite, and above 0: 0 times it stays 0, an infinity one
   p.mult = copysignf(fminf(fmaxf(fabsf(p.capped ? scale / a->softcap : scale * kLog2e), 1e-37f),
                            3e38f), scale);
+#ifdef DCP_DEBUG_POISON
+  t.withheld_cta = g_withheld[0], t.withheld_unit = g_withheld[1], t.withheld_copy = g_withheld[2];
+#endif
   if (prepare_device(&t) != cudaSuccess) return DCP_ERR_CUDA;
   const cudaStream_t st = (cudaStream_t)stream;
   return a->dim == 64    ? launch_tiles<64>(a, t, st)
          : a->dim == 128 ? launch_tiles<128>(a, t, st)
                          : launch_tiles<256>(a, t, st);
 }
+
+#ifdef DCP_DEBUG_POISON
+// Race-check build: from now on the given CTA does not bring in the given copy (K
+// or V of a step, in the order of use) of its given unit (-1: none), so that the
+// waits for it run out, after a limit that is short in this build.
+extern "C" void dcp_prompt_selftest_withhold(int cta, int unit, int copy) {
+  g_withheld[0] = cta, g_withheld[1] = unit, g_withheld[2] = copy;
+}
+#endif

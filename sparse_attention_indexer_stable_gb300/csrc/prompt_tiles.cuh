@@ -91,7 +91,7 @@ struct alignas(1024) Shared {
   unsigned long long turn[S::kTiles];
   Unit unit[kRing];
   uint32_t tmem;
-  int given_up;
+  int given_up, beats;  // see Patience
 };
 
 struct TileParams {
@@ -102,6 +102,9 @@ struct TileParams {
   int sets;    // of packed heads: kv_heads * group / packed
   int sms;
   uint32_t q_bytes;  // of a tile's copy
+#ifdef DCP_DEBUG_POISON
+  int withheld_cta, withheld_unit, withheld_copy;  // see dcp_prompt_selftest_withhold
+#endif
   int out_box;       // whether 32 of a tile's rows are a box of the output
 };
 
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         mbar_init(&s.o_read[t], 4);
         mbar_init(&s.turn[t], 1);
       }
-      s.given_up = 0;
+      s.given_up = s.beats = 0;
       mbar_fence_init();
     }
     __syncwarp();
@@ -288,13 +291,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
 
+  const Patience patience{&s.given_up, &s.beats, a.status};
   // A wait of a whole warp.
   auto wait = [&](unsigned long long* bar, uint32_t parity) {
-    return __all_sync(~0u, wait_for(bar, parity, &s.given_up, a.status)) != 0;
+    return __all_sync(~0u, wait_for(bar, parity, patience)) != 0;
   };
   // The k-th unit.  All roles take all units, even when the CTA has given up.
   auto unit_at = [&](int k, Unit* u) {
-    if (!mbar_wait_bounded(&s.unit_full[k % kRing], (k / kRing) & 1, 2 * kPatience))
+    if (!__all_sync(~0u, outlast(&s.unit_full[k % kRing], (k / kRing) & 1, patience)))
       return false;
     *u = s.unit[k % kRing];
     return u->q0 >= 0;
@@ -319,8 +323,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll 1
       for (int k = 0;;) {
         // whether the CTA has given up or not: what was taken has to be handed on
-        if (k >= kRing &&
-            !mbar_wait_bounded(&s.unit_empty[k % kRing], (k / kRing - 1) & 1, 2 * kPatience))
+        if (k >= kRing && !__all_sync(~0u, outlast(&s.unit_empty[k % kRing], (k / kRing - 1) & 1,
+                                                   patience)))
           break;
         if (!here && more && !s.given_up) {
           uint32_t taken = 0, x = 0;
@@ -374,8 +378,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           if (!w.steps[t]) continue;
-          ok = ok && (q_round[t] == 0 || wait_for(&s.q_empty[t], (q_round[t] - 1) & 1, &s.given_up,
-                                                  a.status));
+          ok = ok && (q_round[t] == 0 || wait_for(&s.q_empty[t], (q_round[t] - 1) & 1, patience));
           if (!ok) break;
           ++q_round[t];
           mbar_expect_tx(&s.q_full[t], a.q_bytes);
@@ -393,10 +396,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll 1
           for (int part = 0; part < kParts; ++part) {
             const int slot = at % kStages, round = at / kStages;
-            ok = round == 0 || wait_for(&s.empty[slot], (round - 1) & 1, &s.given_up, a.status);
+            ok = round == 0 || wait_for(&s.empty[slot], (round - 1) & 1, patience);
             if (!ok) break;
             ++at;
             mbar_expect_tx(&s.full[slot], Sh::kStageBytes);
+#ifdef DCP_DEBUG_POISON
+            if ((int)blockIdx.x == a.withheld_cta && k == a.withheld_unit && i == a.withheld_copy)
+              continue;
+#endif
             for (int c = 0; c < Sh::kPartChunks; ++c)
               tensor_load_3d(s.stage[slot] + c * kKeys * 128, value ? &v_map : &k_map,
                              (part * Sh::kPartChunks + c) * 64, w.kv,
@@ -407,9 +414,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       if (lane == 0 && s.given_up) {  // copies in flight, each for a limited time
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
-          if (q_round[t]) mbar_wait_bounded(&s.q_full[t], (q_round[t] - 1) & 1, kPatience);
+          if (q_round[t]) outlast(&s.q_full[t], (q_round[t] - 1) & 1, patience);
         for (int i = max(0, at - kStages); i < at; ++i)
-          mbar_wait_bounded(&s.full[i % kStages], (i / kStages) & 1, kPatience);
+          outlast(&s.full[i % kStages], (i / kStages) & 1, patience);
       }
       __syncwarp();
     } else if (warp == Sh::kRowWarps || (kTiles == 2 && warp == Sh::kRowWarps + 3)) {
@@ -585,7 +592,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       }
       // products in flight, and the arrivals that they owe, for a limited time
       if (leader) mma_commit(&s.drained[t]);
-      mbar_wait_bounded(&s.drained[t], 0, kPatience);
+      outlast(&s.drained[t], 0, patience);
       __syncwarp();
     }
   } else {
@@ -617,7 +624,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     // Waits that have given up end at once: the rest of the unit is computed on
     // whatever there is, and becomes NaN.
     auto wait_here = [&](unsigned long long* bar, uint32_t parity) {
-      wait_for(bar, parity, &s.given_up, a.status);
+      wait_for(bar, parity, patience);
       __syncwarp();
       tmem_fence_after();
     };
@@ -855,6 +862,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         const int r = __ffs(again) - 1;
         again &= again - 1;
         attend_row_again<D>(p, u.first, u.n, __shfl_sync(~0u, i, r), __shfl_sync(~0u, head, r));
+        if (lane == 0) atomicAdd(&s.beats, 1);
       }
     }
   }

@@ -204,27 +204,57 @@ __device__ __forceinline__ void async_proxy_fence() {
 }
 
 // -------------------------------------------------------------------- waits
-// The first wait of a CTA that takes longer than about a second sets `given_up`
-// and the device's status bit; all later ones end at once.
-constexpr unsigned long long kPatience = 2000000000ull;  // SM clocks
+// A CTA's waits end.  The first one that takes longer than about a second sets
+// `given_up` and the device's status bit; all later ones then end at once.  Slow
+// work that others wait for counts `beats`, from each of which the second begins
+// anew.
+#ifdef DCP_DEBUG_POISON
+constexpr unsigned long long kPatience = 4000000ull;  // SM clocks: about 2 ms
+#else
+constexpr unsigned long long kPatience = 2000000000ull;
+#endif
 
-__device__ __forceinline__ bool wait_long(unsigned long long* bar, uint32_t parity,
-                                       volatile int* given_up, unsigned int* status) {
-  const unsigned long long t0 = clock64();
+struct Patience {
+  volatile int* given_up;
+  volatile int* beats;
+  unsigned int* status;
+};
+
+// Whether phase `parity` of `bar` completes before the CTA gives up.
+__device__ __forceinline__ bool wait_for(unsigned long long* bar, uint32_t parity,
+                                         const Patience& w) {
+  if (mbar_try_wait(bar, parity)) return true;
+  unsigned long long t0 = clock64();
+  int seen = *w.beats;
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*given_up) return false;
+    if (*w.given_up) return false;
     if (clock64() - t0 > kPatience) {
-      *given_up = 1;
-      atomicOr(status, kStatusCopyTimeout);
-      return false;
+      if (*w.beats == seen) break;
+      t0 = clock64();
+      seen = *w.beats;
     }
   }
+  *w.given_up = 1;
+  atomicOr(w.status, kStatusCopyTimeout);
+  return false;
 }
-__device__ __forceinline__ bool wait_for(unsigned long long* bar, uint32_t parity,
-                                         volatile int* given_up, unsigned int* status) {
+
+// The same for what has to be waited for even when the CTA has given up; twice
+// as long, so that it is not what gives up first.
+__device__ __forceinline__ bool outlast(unsigned long long* bar, uint32_t parity,
+                                        const Patience& w) {
   if (mbar_try_wait(bar, parity)) return true;
-  return wait_long(bar, parity, given_up, status);
+  unsigned long long t0 = clock64();
+  int seen = *w.beats;
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (clock64() - t0 > 2 * kPatience) {
+      if (*w.beats == seen) return false;
+      t0 = clock64();
+      seen = *w.beats;
+    }
+  }
 }
 
 }  // namespace dcp

@@ -117,32 +117,36 @@ struct Finder {
   int behind = 0, here = 0;  // units of later blocks, and of this one
   int base = 0, passed = 0;  // this block's units in the sequences before base
   int total = -1;            // units, once known
+  int kept = 0;              // blocks of the lane's sequence of the first 32
 
   __device__ int blocks(const Params& p, int tokens, int b) const {
     if (b >= p.num_seqs) return 0;
     const int n = start_of(p, b + 1) - start_of(p, b);
     return n > 0 ? (n + tokens - 1) / tokens : 0;
   }
+  __device__ void begin(const Params& p, int tokens) {
+    kept = blocks(p, tokens, threadIdx.x & 31);
+  }
   // units whose block is `from` or later
   __device__ int count(const Params& p, int tokens, int from) const {
-    int c = 0;
+    int c = max(0, kept - from);
 #pragma unroll 1
-    for (int b = threadIdx.x & 31; b < p.num_seqs; b += 32)
+    for (int b = 32 + (threadIdx.x & 31); b < p.num_seqs; b += 32)
       c += max(0, blocks(p, tokens, b) - from);
     return __reduce_add_sync(~0u, c);
   }
 
   __device__ __forceinline__ Unit find(const Params& p, int tokens, int u) {
     const int lane = threadIdx.x & 31;
-    if (u < behind + passed) *this = Finder();
+    if (u < behind + passed) level = -1, behind = here = base = passed = 0;
     if (total < 0) total = count(p, tokens, 0);
     if (u >= total) return Unit{0, 0, -1, 0};
     if (level < 0 || u >= behind + here) {
       int lo = 0, hi = level, at_hi = behind, at_lo = total;
       if (level < 0) {
-        hi = 0;
+        hi = kept;
 #pragma unroll 1
-        for (int b = lane; b < p.num_seqs; b += 32) hi = max(hi, blocks(p, tokens, b));
+        for (int b = 32 + lane; b < p.num_seqs; b += 32) hi = max(hi, blocks(p, tokens, b));
         hi = __reduce_max_sync(~0u, hi);
       } else {
         at_hi += here;
@@ -157,7 +161,7 @@ struct Finder {
     }
 #pragma unroll 1
     for (; base < p.num_seqs; base += 32) {
-      const unsigned has = __ballot_sync(~0u, blocks(p, tokens, base + lane) > level);
+      const unsigned has = __ballot_sync(~0u, (base ? blocks(p, tokens, base + lane) : kept) > level);
       const int left = u - behind - passed;
       if (left < __popc(has)) {
         const int b = base + __fns(has, 0, left + 1);
@@ -286,6 +290,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     __syncwarp();
   }
   if (warp == Sh::kRowWarps) tmem_allocate(&s.tmem, Sh::kColumns);
+  Finder finder;
+  if (warp == Sh::kRowWarps + 2) finder.begin(p, kTiles * a.tokens);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -316,7 +322,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       // This CTA's, then those of CTAs that have not started.  No more are taken
       // than the SMs cannot begin at once; what the grid has beyond the last unit
       // is taken too and needs no CTA.
-      Finder finder;
       uint32_t index = blockIdx.x;
       bool here = true, more = gridDim.x > (unsigned)a.sms;
       int fetches = 0;
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       }
       // products in flight, and the arrivals that they owe, for a limited time
       if (leader) mma_commit(&s.drained[t]);
-      outlast(&s.drained[t], 0, patience);
+      if (!outlast(&s.drained[t], 0, patience)) *patience.given_up = 1;
       __syncwarp();
     }
   } else {
@@ -621,13 +626,18 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       if (lane == 0) mbar_arrive(bar);
     };
     int s_round = 0, o_round = 0;  // phases of s_full and o_done
-    // Waits that have given up end at once: the rest of the unit is computed on
-    // whatever there is, and becomes NaN.
+    // What the rows wait for depends on warps whose waits end.  When the CTA has
+    // given up the rest of the unit is computed on whatever there is, and becomes
+    // NaN.
     auto wait_here = [&](unsigned long long* bar, uint32_t parity) {
-      wait_for(bar, parity, patience);
+      while (!mbar_try_wait(bar, parity) && !*patience.given_up) {
+      }
       __syncwarp();
       tmem_fence_after();
     };
+    // the warp's first row, as a box of the output has it
+    const int box_token = 32 * (warp & 3) / a.packed;
+    const int box_head = 32 * (warp & 3) - box_token * a.packed;
     Unit u;
     for (int k = 0; unit_at(k, &u); unit_done(k++)) {
       const Walk<D> w(a, u);
@@ -832,9 +842,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           async_proxy_fence();
           __syncwarp();
           if (lane == 0) {
-            const int first_row = 32 * (warp & 3), in_tile = first_row / a.packed;
-            tensor_store_3d(&out_map, s.rows[warp], c, w.head0 + first_row - in_tile * a.packed,
-                            u.first + u.q0 + t * a.tokens + in_tile);
+            tensor_store_3d(&out_map, s.rows[warp], c, w.head0 + box_head,
+                            u.first + u.q0 + t * a.tokens + box_token);
             bulk_commit();
           }
           continue;

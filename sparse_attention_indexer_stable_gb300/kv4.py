@@ -159,7 +159,7 @@ def kv4_extend(table, lens, counts, free, used, places, page_size, num_pages, ou
                                    out, _handle(stream))
     if type(r) is int:
         _raise(r, "dcp_kv4_extend")
-    return Kv4Step._make(r)
+    return tuple.__new__(Kv4Step, r)
 
 
 def kv4_append(cache, k, v, slots, stream=None):

@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   Shared<D>& s = *reinterpret_cast<Shared<D>*>(((uintptr_t)tiles_smem + 1023) & ~(uintptr_t)1023);
   const Params& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  kv4::grid_dependency_wait();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == Sh::kRowWarps) {
     if (lane == 0) {
@@ -295,6 +295,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  // Only now, with its tensor memory, does the CTA let the stream's next kernel be
+  // scheduled: one that took some first and then waited for this one would stop it.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = s.tmem;
 
   const Patience patience{&s.given_up, &s.beats, a.status};
@@ -551,8 +554,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           ok = ok && arrived(v_at);
           if (!ok) break;
           if (j < steps) {
-            // rows of this step behind the last sequence
-            const int inside = rows_end - u.first - w.from - j * kKeys;
+            // rows of this step behind the last sequence (none before it, unless
+            // starts does not ascend)
+            const int inside = max(0, rows_end - u.first - w.from - j * kKeys);
             if (inside < kKeys) {
               for (int c = 0; c < Sh::kChunks; ++c)
                 for (int i = inside * 8 + lane; i < kKeys * 8; i += 32)

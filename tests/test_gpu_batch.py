@@ -59,7 +59,7 @@ def check_extend(dk, table, lens, counts, free, used, places, page, num_pages, p
 
 @pytest.mark.parametrize("B,page,longest,most,extra", [
     (1, 1, 0, 1, 0), (1, 64, 100, 1, 0), (3, 16, 40, 50, 5), (7, 2, 9, 3, 1), (33, 64, 300, 200, 0),
-    (1025, 16, 90, 1, 30), (2500, 4, 20, 9, 0), (5, 128, 1000, 3000, 100), (2, 65536, 70000, 9, 0)])
+    (1025, 16, 90, 1, 30), (2500, 4, 20, 9, 0), (16384, 8, 20, 2, 100), (5, 128, 1000, 3000, 100), (2, 65536, 70000, 9, 0)])
 def test_extend_matches_the_definition(dk, B, page, longest, most, extra):
     rng = np.random.default_rng(B * page)
     table, lens, counts, free, pages = batch(rng, B, page, longest, most)
@@ -141,6 +141,21 @@ def test_extend_in_place_through_a_graph(dk):
         host = (np.array(want[7]), want[5], want[6])
 
 
+@pytest.mark.parametrize("B,most", [(40, 300), (1500, 9), (3, 30000)])
+def test_extend_in_place_with_many_places(dk, B, most):
+    """Lengths and the list's count in place, over all CTAs of a cluster."""
+    rng = np.random.default_rng(B)
+    table, lens, counts, free, pages = batch(rng, B, 16, 100, most)
+    places = int(counts.sum()) + 50
+    t, n, u = i32(table), i32(lens), i32([0])
+    step = dk.Kv4Step(torch.empty(places, dtype=torch.int64, device=DEV), *[
+        torch.empty(places, dtype=torch.int32, device=DEV) for _ in range(3)],
+        torch.empty(B + 1, dtype=torch.int32, device=DEV), n, u)
+    dk.kv4_extend(t, n, i32(counts), i32(free), u, places, 16, pages, out=step)
+    want = ref.extend(table, lens, counts, free, 0, places, 16, pages)
+    assert [x.tolist() for x in step] == list(want[:7]) and t.tolist() == want[7]
+
+
 def test_extend_on_another_stream(dk):
     rng = np.random.default_rng(2)
     table, lens, counts, free, pages = batch(rng, 20, 16, 200, 100)
@@ -211,7 +226,8 @@ def check_turned(rope, got, x, positions, dtype):
 @pytest.mark.parametrize("n,hq,hk,D,R,layout", [
     (1, 1, 1, 64, 64, "plain"), (5, 8, 2, 128, 128, "sliced"), (3, 3, 1, 128, 64, "odd"),
     (33, 12, 12, 64, 32, "heads first"), (2, 4, 1, 256, 256, "plain"), (7, 2, 1, 96, 2, "plain"),
-    (4, 5, 5, 80, 48, "sliced"), (1, 40, 8, 1024, 1024, "plain"), (9, 1, 1, 7, 6, "plain")])
+    (4, 5, 5, 80, 48, "sliced"), (1, 40, 8, 1024, 1024, "plain"), (9, 1, 1, 7, 6, "plain"),
+    (2, 60, 10, 1023, 1022, "plain"), (3, 600, 1, 128, 128, "plain")])
 def test_rotary_matches_the_definition(dk, dtype, interleaved, n, hq, hk, D, R, layout):
     rng = np.random.default_rng(n * D + R)
     rope = dk.Rotary(R, interleaved=interleaved)

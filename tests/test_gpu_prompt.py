@@ -137,8 +137,12 @@ def test_starts_outside_the_rows_are_cut(dk):
     want, want_lse = dk.prompt_attention(q, k, v, torch.tensor([0, 100, 300], device=DEV).int())
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     # no order: any result, but nothing is touched outside
-    dk.prompt_attention(q, k, v, torch.tensor([200, 10, 250, -3, 2 ** 31 - 1], device=DEV).int())
+    for starts in ([200, 10, 250, -3, 2 ** 31 - 1], [0, 300, 5], [300, 0], [10, 290, 0, 300, 1]):
+        for causal in (True, False):
+            dk.prompt_attention(q, k, v, torch.tensor(starts, device=DEV).int(), causal=causal)
     torch.cuda.synchronize()
+    again, again_lse = dk.prompt_attention(q, k, v, torch.tensor([0, 100, 300], device=DEV).int())
+    assert torch.equal(again, want) and torch.equal(again_lse, want_lse)
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])

@@ -2,8 +2,8 @@
 
 The compute lives in ``_build/libdcp_topk.so`` (CUDA, sm_103a), declared in
 ``include/dcp_topk.h``, ``include/dcp_kv4.h`` and ``include/dcp_prompt.h``.  This module only
-marshals torch tensors (device memory) and the current CUDA stream into that ABI; every step of the top-K
-runs in the library's kernels.  There is no CPU fallback: if the library is
+marshals torch tensors (device memory) and the current CUDA stream into that ABI; every step of
+the top-K runs in the library's kernels.  There is no CPU fallback: if the library is
 missing or fails to load, every call raises.
 
 Functions with the ABI's names take raw device pointers and sizes, exactly like

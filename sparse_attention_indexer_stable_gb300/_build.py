@@ -1,5 +1,6 @@
 """Builds the CUDA library in-tree: csrc/*.cu -> _build/libdcp_topk.so (sm_103a),
-and the torch side of the 4-bit cache and its prompts: csrc/kv4_binding.cpp -> _build/_kv4_binding-*.so.
+and the torch side of the 4-bit cache and its prompts: csrc/kv4_binding.cpp ->
+_build/_kv4_binding-*.so.
 
 Plain nvcc, one translation unit per subject compiled side by side, no CMake; host code has no
 architecture-specific flags so the same source builds on x86_64 and aarch64.

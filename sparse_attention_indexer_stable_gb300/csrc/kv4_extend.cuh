@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(kExtendThreads, 1) extend_kernel(const ExtendP
           if (from < p.num_free) page = p.free_pages[from];
           if ((at & (size - 1)) == 0) *entry = page;  // the page's first token
         }
-        if ((uint32_t)page < p.num_pages) slot = ((int64_t)page << p.page_shift) + (at & (size - 1));
+        if ((uint32_t)page < p.num_pages)
+          slot = ((int64_t)page << p.page_shift) + (at & (size - 1));
       }
     }
     p.slots[t] = slot;

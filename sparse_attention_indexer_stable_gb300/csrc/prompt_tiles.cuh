@@ -169,7 +169,8 @@ struct Finder {
     }
 #pragma unroll 1
     for (; base < p.num_seqs; base += 32) {
-      const unsigned has = __ballot_sync(~0u, (base ? blocks(p, tokens, base + lane) : kept) > level);
+      const unsigned has =
+          __ballot_sync(~0u, (base ? blocks(p, tokens, base + lane) : kept) > level);
       const int left = u - behind - passed;
       if (left < __popc(has)) {
         const int b = base + __fns(has, 0, left + 1);
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
           for (int i = 0; i < Sh::kPart / 16; ++i) {
             if (leader)
               mma_smem(s_at,
-                       q_rows + ((part * Sh::kPartChunks + i / 4) * kTileRows * 128 + i % 4 * 32) / 16,
+                       q_rows + (part * Sh::kPartChunks + i / 4) * (kTileRows * 8) + i % 4 * 2,
                        rows + (i / 4 * kKeys * 128 + i % 4 * 32) / 16, scores, part > 0 || i > 0);
           }
           if (part + 1 < kParts) free_part(g, part);
@@ -711,8 +712,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
         // Caps and masks: in tensor memory, in a loop.  (Unrolled over the registers
         // they were so much code that instructions came from the second-level
         // cache: with caps 1977 us instead of 577, without 419 instead of 317, for 33
-        // prompts of 2048 rows with a window of 1000.)
-        if (kCapped || __builtin_expect(edge, 0)) {
+        // prompts of 2048 rows with a window of 1000.  Caps by 32 scores: 546 us
+        // for prompts of 1 to 4097 rows, by 16 586; but 597 and 552 where one score in
+        // some hundred is beyond the cap.)
+        auto finish_scores = [&] {
           constexpr int kPiece = kCapped ? 32 : 16;
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += kPiece) {
@@ -720,11 +723,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
             if (!kCapped && inside) continue;
             uint32_t piece[kPiece];
             float* y = reinterpret_cast<float*>(piece);
+            auto put = [&] {
+              if constexpr (kCapped) tmem_store32(s_at + c, piece);
+              else tmem_store16(s_at + c, piece);
+            };
             if (base + c >= most_hi || base + c + kPiece <= least_lo) {
 #pragma unroll
               for (int e = 0; e < kPiece; ++e) y[e] = -INFINITY;
-              if constexpr (kCapped) tmem_store32(s_at + c, piece);
-              else tmem_store16(s_at + c, piece);
+              put();
               continue;
             }
             if constexpr (kCapped) tmem_load32(s_at + c, piece);
@@ -736,10 +742,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
                 for (int e = 0; e < kPiece; ++e)
                   if (e < from || e >= to) y[e] = 0.0f;
               }
-              float most = 0.0f;
+              float most[4] = {};
 #pragma unroll
-              for (int e = 0; e < kPiece; e += 2) most = max3(most, fabsf(y[e]), fabsf(y[e + 1]));
-              if (__all_sync(~0u, most * mult <= 1.0f)) {
+              for (int e = 0; e < kPiece; e += 8)
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                  most[f] = max3(most[f], fabsf(y[e + 2 * f]), fabsf(y[e + 2 * f + 1]));
+              const float top = fmaxf(max3(most[0], most[1], most[2]), most[3]);
+              if (__all_sync(~0u, top * mult <= 1.0f)) {
 #pragma unroll
                 for (int e = 0; e < kPiece; e += 2) {
                   const float2 u = mul2(make_float2(y[e], y[e + 1]), make_float2(mult, mult));
@@ -761,12 +771,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
               for (int e = 0; e < kPiece; ++e)
                 if (e < from || e >= to) y[e] = -INFINITY;
             }
-            if constexpr (kCapped) tmem_store32(s_at + c, piece);
-            else tmem_store16(s_at + c, piece);
+            put();
           }
           tmem_wait_store();
-        }
-        tmem_load128(s_at, raw);
+          tmem_load128(s_at, raw);
+        };
+        if (!kCapped && __builtin_expect(!edge, 1)) tmem_load128(s_at, raw);
+        else finish_scores();
         float sum = 0.0f;
         bool good = false;
         if (__builtin_expect(j > 0, 1)) {

@@ -2,12 +2,12 @@
 ABI of include/dcp_kv4.h.
 
 ``Kv4Cache`` is a handle on four torch tensors (codes and scales of K and V in
-pages); ``kv4_extend`` gives a batch's new tokens pages and slots, ``kv4_append`` and ``kv4_read`` write tokens and read them back,
-``kv4_attention`` attends over every visible position of a row or over the ids
-that ``merge`` and ``fused_topk`` give, ``kv4_evict`` keeps a sequence's
-heaviest tokens.  As in the rest of the package all the work runs in the
-library's kernels on the current CUDA stream (or on ``stream=``), nothing
-synchronises the host, and there is no CPU fallback.
+pages); ``kv4_extend`` gives a batch's new tokens pages and slots, ``kv4_append``
+and ``kv4_read`` write tokens and read them back, ``kv4_attention`` attends over
+every visible position of a row or over the ids that ``merge`` and ``fused_topk``
+give, ``kv4_evict`` keeps a sequence's heaviest tokens.  As in the rest of the
+package all the work runs in the library's kernels on the current CUDA stream (or
+on ``stream=``), nothing synchronises the host, and there is no CPU fallback.
 """
 from __future__ import annotations
 
@@ -20,8 +20,8 @@ from typing import Any, NamedTuple
 
 from . import DCP_OK, DcpError, _build, _check, _torch, library
 
-__all__ = ["Kv4Cache", "Kv4Step", "kv4_extend", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_workspace_size",
-           "kv4_evict", "DCP_F16", "DCP_BF16", "DCP_F32"]
+__all__ = ["Kv4Cache", "Kv4Step", "kv4_extend", "kv4_append", "kv4_read", "kv4_attention",
+           "kv4_attention_workspace_size", "kv4_evict", "DCP_F16", "DCP_BF16", "DCP_F32"]
 
 DCP_F16, DCP_BF16, DCP_F32 = 0, 1, 2
 

@@ -59,7 +59,8 @@ def check_extend(dk, table, lens, counts, free, used, places, page, num_pages, p
 
 @pytest.mark.parametrize("B,page,longest,most,extra", [
     (1, 1, 0, 1, 0), (1, 64, 100, 1, 0), (3, 16, 40, 50, 5), (7, 2, 9, 3, 1), (33, 64, 300, 200, 0),
-    (1025, 16, 90, 1, 30), (2500, 4, 20, 9, 0), (16384, 8, 20, 2, 100), (5, 128, 1000, 3000, 100), (2, 65536, 70000, 9, 0)])
+    (1025, 16, 90, 1, 30), (2500, 4, 20, 9, 0), (16384, 8, 20, 2, 100), (5, 128, 1000, 3000, 100),
+    (2, 65536, 70000, 9, 0)])
 def test_extend_matches_the_definition(dk, B, page, longest, most, extra):
     rng = np.random.default_rng(B * page)
     table, lens, counts, free, pages = batch(rng, B, page, longest, most)

@@ -207,7 +207,8 @@ def test_huge_scores_stay_finite(dk):
     """Scores far beyond the exponent's range on both sides."""
     for dim in (64, 128, 256):
         q, k, v = inputs(14, 300, 1, 4, dim, "bf16", size=300.0)
-        out, lse = dk.prompt_attention(q, k, v, torch.tensor([0, 300], device=DEV).int(), scale=40.0)
+        out, lse = dk.prompt_attention(q, k, v, torch.tensor([0, 300], device=DEV).int(),
+                                       scale=40.0)
         assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
 
 

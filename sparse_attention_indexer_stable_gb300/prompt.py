@@ -13,8 +13,8 @@ from __future__ import annotations
 import math
 from fractions import Fraction
 
-from . import _torch
-from .kv4 import _bind, _handle, _raise
+from . import _torch, kv4
+from .kv4 import _handle, _raise
 
 __all__ = ["Rotary", "rotary", "prompt_attention"]
 
@@ -91,8 +91,9 @@ def rotary(rope, positions, q, k=None, q_out=None, k_out=None, stream=None):
     """
     if not isinstance(rope, Rotary):
         raise TypeError("rope must be a Rotary")
-    r = _bind().rotary(rope.turns, rope.dim, rope.interleaved, rope.magnitude, positions, q, k,
-                       q_out, k_out, _handle(stream))
+    r = (kv4._bound or kv4._bind()).rotary(rope.turns, rope.dim, rope.interleaved,
+                                               rope.magnitude, positions, q, k, q_out, k_out,
+                                               _handle(stream))
     if type(r) is int:
         _raise(r, "dcp_rotary")
     return r
@@ -115,8 +116,8 @@ def prompt_attention(q, k, v, starts, causal=True, window=0, scale=None, softcap
     Rows of no sequence are left as they are in out and lse; where these are
     allocated here, such rows hold no particular value.
     """
-    r = _bind().prompt_attention(q, k, v, starts, causal, window, scale, softcap, out, lse,
-                                 _handle(stream))
+    r = (kv4._bound or kv4._bind()).prompt_attention(q, k, v, starts, causal, window, scale,
+                                                     softcap, out, lse, _handle(stream))
     if type(r) is int:
         _raise(r, "dcp_prompt_attention")
     return r

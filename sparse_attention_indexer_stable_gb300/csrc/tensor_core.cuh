@@ -242,7 +242,7 @@ __device__ __forceinline__ bool wait_for(unsigned long long* bar, uint32_t parit
 }
 
 // The same for what has to be waited for even when the CTA has given up; twice
-// as long, so that it is not what gives up first.
+// as long, so that it is not what gives up first, as it then does too.
 __device__ __forceinline__ bool outlast(unsigned long long* bar, uint32_t parity,
                                         const Patience& w) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -251,11 +251,14 @@ __device__ __forceinline__ bool outlast(unsigned long long* bar, uint32_t parity
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
     if (clock64() - t0 > 2 * kPatience) {
-      if (*w.beats == seen) return false;
+      if (*w.beats == seen) break;
       t0 = clock64();
       seen = *w.beats;
     }
   }
+  *w.given_up = 1;
+  atomicOr(w.status, kStatusCopyTimeout);
+  return false;
 }
 
 }  // namespace dcp

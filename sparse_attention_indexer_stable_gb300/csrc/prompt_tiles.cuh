@@ -31,8 +31,8 @@
 //   one a tile's products, so that the next unit's copies and first S overlap the
 //   last one's end.
 //
-// Measured: one prompt of 16384 rows, 64 heads of 128 over 8: 2650 us, 1.66 PFLOP/s,
-// 86% of the measured matrix rate; a step of both tiles takes 2500 to 3200 cycles,
+// Measured: one prompt of 16384 rows, 64 heads of 128 over 8: 2749 us, 1.60 PFLOP/s,
+// 83% of the measured matrix rate; a step of both tiles takes 2500 to 3200 cycles,
 // its products 2048.
 //
 // Masked scores are -infinity and their P is 0, but 0 times an infinite or NaN

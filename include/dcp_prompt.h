@@ -77,7 +77,9 @@ dcp_status dcp_rotary(const dcp_rotary_args* args, dcp_stream_t stream);
  *
  * Products of the inputs are exact and summed in fp32; the probabilities are
  * rounded to dtype for the second product only, their sum is kept in fp32
- * (compensated).  What a row does not see has no influence on it, whatever its
+ * (compensated).  Scores may be of any size, as long as q . k_j and s_j / ln 2
+ * are finite in fp32; rows with a largest score beyond 2^20 ln 2 are computed on
+ * the plain units, about a thousand times slower.  What a row does not see has no influence on it, whatever its
  * value (infinities and NaN too).  Rows of no sequence are neither read nor
  * written.  starts ascends from 0 or more to at most rows; values outside are
  * cut there.

@@ -37,7 +37,8 @@
 //
 // Masked scores are -infinity and their P is 0, but 0 times an infinite or NaN
 // value is NaN: rows whose O is not finite although their sum is are computed
-// again by attend_row, which reads only what a row sees.  Values behind the
+// again by attend_row, which reads only what a row sees (as are rows whose scores
+// are too large for the exponents' way of rounding, see kFar).  Values behind the
 // last sequence, where there may be anything, become zeros before the product.
 #pragma once
 
@@ -631,6 +632,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
     // none is too large
     constexpr float kBelow = kHalf ? 4.0f : 0.0f, kMost = kHalf ? 15.0f : 60.0f;
     constexpr float kLargest = kHalf ? 0x1p15f : 0x1p60f;
+    // The exponent takes the exact product of score and mult, the reference is a
+    // rounded one: P of the maximum itself is off by 2^(half a step of the
+    // reference).  Up to here that is 2^(2^-4); from 2^30 on the only P may be 0.
+    // Rows whose last reference lies beyond are computed again by attend_row, whose
+    // products are all rounded.  (Multiplying such rows' scores before, beside
+    // others in the same warp, cost heads of 64 5%.)
+    constexpr float kFar = 0x1p20f;
     auto arrive = [&](unsigned long long* bar) {
       tmem_fence_before();
       __syncwarp();
@@ -792,8 +800,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
             const float next = top - kBelow;
             shrink = exp2f(ref - next);  // 0 at first
             ref = next;
-            l *= shrink;
-            over *= shrink;
+            // nothing is left of the sum, even if it was infinite (kFar)
+            l = shrink > 0.0f ? l * shrink : 0.0f;
+            over = shrink > 0.0f ? over * shrink : 0.0f;
           }
           if (j > 0) {
             wait_last();
@@ -883,7 +892,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
       const float2 none = add2(zero[0], zero[1]);
       const bool finite = none.x + none.y == 0.0f;
       // a NaN among the scores that the row sees makes the sum NaN, and is right
-      unsigned again = __ballot_sync(~0u, ok && valid && !finite && l == l);
+      const bool far = !kCapped && fabsf(ref) > kFar && fabsf(ref) < INFINITY;
+      unsigned again = __ballot_sync(~0u, ok && valid && (far || (!finite && l == l)));
       if (again) {
         if (lane == 0) bulk_wait();  // those rows are written once more
         __syncwarp();

@@ -79,14 +79,20 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// tanh by 1 - 2 / (e^2x + 1), and near 0, where that cancels, by the odd
-// series to x^9: relative error below 2^-20 (the series' at 0.35 2^-21, the
-// quotient's approximations 2^-22 of 1).
+// tanh by 1 - 2 / (e^2x + 1), for x away from 0, where that cancels.
+__device__ __forceinline__ float tanh_far(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;"
+      : "=f"(r)
+      : "f"(exp2_approx(fabsf(x) * 2.8853900817779268f) + 1.0f));
+  return copysignf(fmaf(-2.0f, r, 1.0f), x);
+}
+
+// tanh, near 0 by the odd series to x^9: relative error below 2^-20 (the series'
+// at 0.35 2^-21, the quotient's approximations 2^-22 of 1).
 __device__ __forceinline__ float tanh_score(float x) {
   const float a = fabsf(x), q = x * x;
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_approx(a * 2.8853900817779268f) + 1.0f));
-  const float far = copysignf(fmaf(-2.0f, r, 1.0f), x);
+  const float far = tanh_far(x);
   float near = fmaf(q, 62.0f / 2835.0f, -17.0f / 315.0f);
   near = fmaf(q, near, 2.0f / 15.0f);
   near = fmaf(q, near, -1.0f / 3.0f);

@@ -42,6 +42,8 @@
 // last sequence, where there may be anything, become zeros before the product.
 #pragma once
 
+#include <type_traits>
+
 #include "prompt_rows.cuh"
 #include "tensor_core.cuh"
 
@@ -755,7 +757,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
                 for (int f = 0; f < 4; ++f)
                   most[f] = max3(most[f], fabsf(y[e + 2 * f]), fabsf(y[e + 2 * f + 1]));
               const float top = fmaxf(max3(most[0], most[1], most[2]), most[3]);
-              if (__all_sync(~0u, top * mult <= 1.0f)) {
+              // Which formula a score takes is its own affair (they differ by their
+              // errors); the warp decides only whether the second one is needed, and
+              // lanes without a row, whose scores may be anything, have no say.
+              const bool some_beyond = __any_sync(~0u, valid && !(top * mult <= 1.0f));
+              auto cap = [&](auto beyond) {
 #pragma unroll
                 for (int e = 0; e < kPiece; e += 2) {
                   const float2 u = mul2(make_float2(y[e], y[e + 1]), make_float2(mult, mult));
@@ -765,12 +771,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
                   for (int i = kTanhTerms - 2; i >= 0; --i)
                     r = fma2(r, square, make_float2(terms[i], terms[i]));
                   r = mul2(r, u);
+                  if constexpr (beyond.value) {
+                    const float2 far = make_float2(p.cap * kv4::tanh_far(u.x), p.cap * kv4::tanh_far(u.y));
+                    r.x = fabsf(u.x) > 1.0f ? far.x : r.x;
+                    r.y = fabsf(u.y) > 1.0f ? far.y : r.y;
+                  }
                   y[e] = r.x, y[e + 1] = r.y;
                 }
-              } else {
-#pragma unroll
-                for (int e = 0; e < kPiece; ++e) y[e] = p.cap * kv4::tanh_score(y[e] * mult);
-              }
+              };
+              if (some_beyond) cap(std::true_type{});
+              else cap(std::false_type{});
             }
             if (!inside) {
 #pragma unroll

@@ -118,3 +118,51 @@ def test_a_maximum_that_travels(dk, dtype, e, dim, order):  # noqa: F811
         # the sum of two products, and what near_score counts
         size = ((q[0, 0].double() * k[best, 0].double()).abs().sum(-1) * dim ** -0.5)[alone, None]
         assert ((lse[alone].double() - want).abs() <= 2.0 ** -20 * size + 2.0 ** -19).all()
+
+
+# -------------------------------------------------------------------- caps
+def fill_shared_memory(dk, dim, value):  # noqa: F811
+    """Leaves `value` as queries in every SM's shared memory."""
+    q = torch.full((256 * 64, 8, dim), value, dtype=torch.bfloat16, device=DEV)
+    dk.prompt_attention(q, q[:, :1], q[:, :1], starts_of(*range(0, 256 * 64 + 1, 256)))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [3, 7, 1])
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+def test_what_shared_memory_held_does_not_matter(dk, dim, group, softcap):  # noqa: F811
+    """Groups that leave a tile's last rows empty, with scores on both sides of
+    the cap: the same bits each time."""
+    q, k, v = inputs(4, 1000, 2, group, dim, "bf16", size=0.1)
+    first = None
+    for value in (0.0, 300.0, float("nan"), 0.0, 1.0):
+        fill_shared_memory(dk, dim, value)
+        got = dk.prompt_attention(q, k, v, starts_of(0, 700, 1000), softcap=softcap)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 3, 8])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=3.0), dict(softcap=3.0, window=70)])
+def test_a_row_does_not_depend_on_others(dk, dim, group, kw):  # noqa: F811
+    """The same bits whatever other heads, later tokens and other sequences hold,
+    on either side of the cap."""
+    n, cut = 500, 333
+    q, k, v = [t.clone() for t in inputs(5, n, 2, group, dim, "bf16", size=0.6)]
+    want = dk.prompt_attention(q, k, v, starts_of(0, cut, n), **kw)
+    # a prompt and its prefix
+    part = dk.prompt_attention(q[:cut - 50], k[:cut - 50], v[:cut - 50], starts_of(0, cut - 50),
+                               **kw)
+    assert all(torch.equal(a[:cut - 50], b) for a, b in zip(want, part))
+    # other queries in later rows and behind the sequence
+    loud = q.clone()
+    loud[200:] *= 50.0
+    got = dk.prompt_attention(loud, k, v, starts_of(0, cut, n), **kw)
+    assert all(torch.equal(a[:200], b[:200]) for a, b in zip(want, got))
+    # other heads
+    if group > 1:
+        loud = q.clone()
+        loud[:, 1::group] *= 50.0
+        got = dk.prompt_attention(loud, k, v, starts_of(0, cut, n), **kw)
+        assert all(torch.equal(a[:, ::group], b[:, ::group]) for a, b in zip(want, got))

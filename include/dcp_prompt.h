@@ -105,8 +105,9 @@ typedef struct {
     int num_seqs;
     int causal;
     int window;             /* 0: none */
-    float scale;            /* 0: dim^-1/2 */
-    float softcap;          /* 0: none */
+    float scale;            /* 0: dim^-1/2; its magnitude is cut to 2^-126 to 2e38 */
+    float softcap;          /* 0, above 2^126 |scale|, or too large to be
+                               divided by ln 2 in fp32: none */
 } dcp_prompt_attention_args;
 
 /*

@@ -2,6 +2,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -171,11 +172,14 @@ extern "C" dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* a,
   p.causal = a->causal != 0;
   p.window = a->window;
   const float scale = a->scale != 0.0f ? a->scale : 1.0f / sqrtf((float)a->dim);
-  p.capped = a->softcap > 0.0f;
-  p.cap = fminf(a->softcap * kLog2e, 3e38f);
+  // A cap that the scores' factor or its own cannot be written beside is so far
+  // away that tanh changes nothing: none.
+  const float ratio = fabsf(scale) / a->softcap;
+  p.capped = a->softcap > 0.0f && ratio >= FLT_MIN && std::isfinite(a->softcap * kLog2e);
+  p.cap = a->softcap * kLog2e;
   // finite, and above 0: 0 times it stays 0, an infinity one
-  p.mult = copysignf(fminf(fmaxf(fabsf(p.capped ? scale / a->softcap : scale * kLog2e), 1e-37f),
-                           3e38f), scale);
+  p.mult = copysignf(fminf(fmaxf(p.capped ? ratio : fabsf(scale) * kLog2e, FLT_MIN), FLT_MAX),
+                     scale);
 #ifdef DCP_DEBUG_POISON
   t.withheld_cta = g_withheld[0], t.withheld_unit = g_withheld[1], t.withheld_copy = g_withheld[2];
 #endif

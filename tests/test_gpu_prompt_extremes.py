@@ -3,6 +3,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from . import prompt_reference as ref  # noqa: E402
 from .test_gpu_prompt import DEV, STEP, dk, inputs  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
@@ -166,3 +167,18 @@ def test_a_row_does_not_depend_on_others(dk, dim, group, kw):  # noqa: F811
         loud[:, 1::group] *= 50.0
         got = dk.prompt_attention(loud, k, v, starts_of(0, cut, n), **kw)
         assert all(torch.equal(a[:, ::group], b[:, ::group]) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("kw", [
+    dict(softcap=1e36), dict(softcap=1e37), dict(softcap=1e38), dict(softcap=3e38),
+    dict(softcap=1e10, scale=1e-30), dict(softcap=3e38, scale=-0.3), dict(softcap=1.0, scale=2e-38)])
+def test_caps_that_are_far_away(dk, dtype, kw):  # noqa: F811
+    """As without one."""
+    for dim in (64, 128):
+        q, k, v = inputs(6, 300, 2, 3, dim, dtype)
+        out, lse = dk.prompt_attention(q, k, v, starts_of(0, 300), **kw)
+        want, want_lse, tol, lse_tol = ref.attention(q, k, v, [0, 300], p_step=STEP[dtype], **kw)
+        assert ((out.double() - want).abs() <= tol + STEP[dtype] * (1 + 2.0 ** -8) * want.abs()
+                + 2.0 ** -25).all()
+        assert ((lse.double() - want_lse).abs() <= lse_tol).all()

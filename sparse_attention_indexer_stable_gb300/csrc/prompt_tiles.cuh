@@ -798,7 +798,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
         bool good = false;
         if (__builtin_expect(j > 0, 1)) {
           sum = exponentials(0);
-          good = sum <= kLargest && maximum(1) <= ref + kMost && ref > -INFINITY;
+          // lanes without a row hold anything, NaN too: no reason for the slow way
+          good = !valid || (sum <= kLargest && maximum(1) <= ref + kMost && ref > -INFINITY);
         }
         if (__builtin_expect(!__all_sync(~0u, good), 0)) {
           if (j > 0) {

@@ -46,9 +46,12 @@ __device__ __forceinline__ float score_of(const Params& p, float dot) {
 }
 
 // Row t (row i of the sequence that starts at row `first` and has n rows), head
-// h, by one warp.
+// h, by one warp.  It counts `beats` (see Patience), since a row of many keys takes
+// longer than those that wait for it would: one every 256 keys, which take some
+// 100 us.
 template <int D>
-__device__ __forceinline__ void attend_row(const Params& p, int first, int n, int i, int h) {
+__device__ __forceinline__ void attend_row(const Params& p, int first, int n, int i, int h,
+                                           int* beats) {
   const int lane = threadIdx.x & 31;
   const int64_t t = first + i;
   const int kv = h / p.group;
@@ -59,6 +62,7 @@ __device__ __forceinline__ void attend_row(const Params& p, int first, int n, in
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
   for (int base = from; base < to; base += 32) {
+    if ((base - from) % 256 == 0 && lane == 0) atomicAdd(beats, 1);
     const int64_t key = (int64_t)first + base + lane;
     const bool sees = base + lane < to;
     float x = -INFINITY;

@@ -219,8 +219,9 @@ __device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
 }
 
 template <int D>
-__device__ __noinline__ void attend_row_again(const Params& p, int first, int n, int i, int h) {
-  attend_row<D>(p, first, n, i, h);
+__device__ __noinline__ void attend_row_again(const Params& p, int first, int n, int i, int h,
+                                              int* beats) {
+  attend_row<D>(p, first, n, i, h, beats);
 }
 
 // The three-input maximum.
@@ -912,8 +913,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
       while (again) {
         const int r = __ffs(again) - 1;
         again &= again - 1;
-        attend_row_again<D>(p, u.first, u.n, __shfl_sync(~0u, i, r), __shfl_sync(~0u, head, r));
-        if (lane == 0) atomicAdd(&s.beats, 1);
+        attend_row_again<D>(p, u.first, u.n, __shfl_sync(~0u, i, r), __shfl_sync(~0u, head, r),
+                            &s.beats);
       }
     }
   }

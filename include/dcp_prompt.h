@@ -79,10 +79,12 @@ dcp_status dcp_rotary(const dcp_rotary_args* args, dcp_stream_t stream);
  * rounded to dtype for the second product only, their sum is kept in fp32
  * (compensated).  Scores may be of any size, as long as q . k_j and s_j / ln 2
  * are finite in fp32; rows with a largest score beyond 2^20 ln 2 are computed on
- * the plain units, about a thousand times slower.  What a row does not see has no influence on it, whatever its
- * value (infinities and NaN too).  Rows of no sequence are neither read nor
- * written.  starts ascends from 0 or more to at most rows; values outside are
- * cut there.
+ * the plain units, some 200 times slower.  What a row does not see has no
+ * influence on it, whatever its value; only, an infinity or NaN among the values
+ * up to 128 rows behind what it sees has it computed on the plain units too, which
+ * round differently within the same bounds.  Rows of no sequence are neither read
+ * nor written.  starts ascends from 0 or more to at most rows; values outside
+ * are cut there.
  */
 typedef struct {
     const void* q;          /* [rows][q_heads][dim] of dtype (fp16 or bf16), dim contiguous */

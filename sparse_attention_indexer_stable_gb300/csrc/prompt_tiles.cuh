@@ -36,10 +36,11 @@
 // its products 2048.
 //
 // Masked scores are -infinity and their P is 0, but 0 times an infinite or NaN
-// value is NaN: rows whose O is not finite although their sum is are computed
-// again by attend_row, which reads only what a row sees (as are rows whose scores
-// are too large for the exponents' way of rounding, see kFar).  Values behind the
-// last sequence, where there may be anything, become zeros before the product.
+// value is NaN: rows whose O is not finite although their sum is are looked at by
+// attend_again, and computed again from what they see alone unless that is what
+// makes them so (as are rows whose scores are too large for the exponents' way of
+// rounding, see kFar).  Values behind the last sequence, where there may be
+// anything, become zeros before the product.
 #pragma once
 
 #include <type_traits>
@@ -216,12 +217,6 @@ __device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
   else
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
-}
-
-template <int D>
-__device__ __noinline__ void attend_row_again(const Params& p, int first, int n, int i, int h,
-                                              int* beats) {
-  attend_row<D>(p, first, n, i, h, beats);
 }
 
 // The three-input maximum.
@@ -904,17 +899,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
       const float2 none = add2(zero[0], zero[1]);
       const bool finite = none.x + none.y == 0.0f;
       // a NaN among the scores that the row sees makes the sum NaN, and is right
-      const bool far = !kCapped && fabsf(ref) > kFar && fabsf(ref) < INFINITY;
-      unsigned again = __ballot_sync(~0u, ok && valid && (far || (!finite && l == l)));
-      if (again) {
-        if (lane == 0) bulk_wait();  // those rows are written once more
+      const unsigned bad = __ballot_sync(~0u, ok && valid && !finite && l == l);
+      const unsigned far = __ballot_sync(
+          ~0u, !kCapped && ok && valid && fabsf(ref) > kFar && fabsf(ref) < INFINITY);
+      if (bad | far) {
+        if (lane == 0) bulk_wait();  // such rows are read, and written once more
         __syncwarp();
-      }
-      while (again) {
-        const int r = __ffs(again) - 1;
-        again &= again - 1;
-        attend_row_again<D>(p, u.first, u.n, __shfl_sync(~0u, i, r), __shfl_sync(~0u, head, r),
-                            &s.beats);
+        attend_again<D, kHalf>(p, u.first, u.n, p.window ? max(0, u.q0 - p.window + 1) : 0,
+                               steps * kKeys, i, head, bad & ~far, far, &s.beats);
       }
     }
   }

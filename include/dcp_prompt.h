@@ -115,7 +115,8 @@ typedef struct {
 /*
  * Errors: DCP_ERR_INVALID for a bad dtype, negative sizes or window, a softcap
  * that is negative, a softcap or scale that is not finite, q_heads not a
- * multiple of kv_heads, or a NULL pointer with rows and num_seqs > 0;
+ * multiple of kv_heads, a NULL pointer with rows and num_seqs > 0, or an out or
+ * lse that shares memory with an input or the other;
  * DCP_ERR_UNSUPPORTED for a dim outside the limits, sizes whose products pass
  * 2^31 - 1 (rows * q_heads), more than 65536 heads, or a q, k or v that tensor
  * copies cannot read: it is not 16-byte aligned, or a stride (of a dimension of

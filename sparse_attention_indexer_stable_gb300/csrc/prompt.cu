@@ -88,6 +88,41 @@ static bool fits(const void* x, int64_t rows, int64_t row_stride, int heads, int
          (heads == 1 || (head_stride > 0 && head_stride < most && head_stride % 8 == 0));
 }
 
+// Whether rows x heads laid out so, `bytes` each, share memory with [begin, end).
+static bool overlaps(const void* x, int64_t rows, int64_t row_stride, int heads,
+                     int64_t head_stride, int64_t bytes, const void* begin, const void* end) {
+  row_stride *= 2, head_stride *= 2;  // bytes
+  const int64_t whole = (rows > 1 ? (rows - 1) * row_stride : 0) +
+                        (heads > 1 ? (heads - 1) * head_stride : 0) + bytes;
+  if (static_cast<const char*>(x) + whole <= begin || x >= end) return false;  // as a rule
+  for (int h = 0; h < heads; ++h) {
+    const char* at = static_cast<const char*>(x) + h * head_stride;
+    // the first row that ends behind `begin`
+    const int64_t before = static_cast<const char*>(begin) - at - bytes;
+    const int64_t row = before < 0 ? 0 : rows == 1 ? 1 : before / row_stride + 1;
+    if (row < rows && at + row * row_stride < static_cast<const char*>(end)) return true;
+  }
+  return false;
+}
+
+// Whether the outputs share memory with each other or with an input.
+static bool outputs_overlap(const dcp_prompt_attention_args* a) {
+  const int64_t bytes = 2 * a->dim, n = a->rows * a->q_heads;
+  const char* begin[2] = {static_cast<const char*>(a->out), reinterpret_cast<const char*>(a->lse)};
+  const char* end[2] = {begin[0] + n * bytes, begin[1] + n * 4};
+  const char* starts = reinterpret_cast<const char*>(a->starts);
+  for (int i = 0; i < 2; ++i)
+    if (overlaps(a->q, a->rows, a->q_row_stride, a->q_heads, a->q_head_stride, bytes, begin[i],
+                 end[i]) ||
+        overlaps(a->k, a->rows, a->k_row_stride, a->kv_heads, a->k_head_stride, bytes, begin[i],
+                 end[i]) ||
+        overlaps(a->v, a->rows, a->v_row_stride, a->kv_heads, a->v_head_stride, bytes, begin[i],
+                 end[i]) ||
+        (starts < end[i] && begin[i] < starts + 4 * ((int64_t)a->num_seqs + 1)))
+      return true;
+  return begin[0] < end[1] && begin[1] < end[0];
+}
+
 // Boxes of `tokens` rows of `packed` heads, 64 elements each.
 static bool map_of(CUtensorMap* map, const void* x, int dtype, int64_t rows, int64_t row_stride,
                    int heads, int64_t head_stride, int dim, int packed, int tokens) {
@@ -154,6 +189,7 @@ extern "C" dcp_status dcp_prompt_attention(const dcp_prompt_attention_args* a,
       !fits(a->k, a->rows, a->k_row_stride, a->kv_heads, a->k_head_stride) ||
       !fits(a->v, a->rows, a->v_row_stride, a->kv_heads, a->v_head_stride))
     return DCP_ERR_UNSUPPORTED;
+  if (outputs_overlap(a)) return DCP_ERR_INVALID;
   TileParams t{};
   Params& p = t.p;
   p.q = a->q, p.k = a->k, p.v = a->v;

@@ -35,6 +35,19 @@ cudaError_t allow_extend() {
   return e;
 }
 
+// The current device's SMs, asked for once.
+cudaError_t count_sms(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if ((*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
+}
+
 // Whether n numbers at a and m at b share memory.
 bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
   return n > 0 && m > 0 && (uintptr_t)a < (uintptr_t)(b + m) && (uintptr_t)b < (uintptr_t)(a + n);
@@ -149,9 +162,11 @@ dcp_status dcp_rotary(const dcp_rotary_args* a, dcp_stream_t stream) {
   p.heads_per_cta = p.heads;
   while ((int64_t)p.heads_per_cta * p.items > 32768) p.heads_per_cta = (p.heads_per_cta + 1) / 2;
   p.per_token = p.heads_per_cta * p.items;
+  int sms;
+  if (count_sms(&sms) != cudaSuccess) return DCP_ERR_CUDA;
   p.tokens_per_cta = 1;
   while (p.tokens_per_cta < 8 && p.tokens_per_cta * p.per_token < 1024 &&
-         a->tokens > (int64_t)p.tokens_per_cta * 8 * 152)
+         a->tokens > (int64_t)p.tokens_per_cta * 8 * sms)
     p.tokens_per_cta *= 2;
   p.by_token = division_by((uint32_t)p.per_token);
   p.by_head = division_by((uint32_t)p.items);

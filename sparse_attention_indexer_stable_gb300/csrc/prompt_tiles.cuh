@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
       const bool leader = elect_one();
       // a negative scale: negated queries
       const uint32_t scores =
-          mma_shape(!kHalf, kTileRows, kKeys, false, false) | (p.mult < 0.0f ? 1u << 13 : 0u);
-      constexpr uint32_t kOuts = mma_shape(!kHalf, kTileRows, Sh::kPart, false, true);
+          mma_shape(!kHalf, kTileRows, kKeys, false) | (p.mult < 0.0f ? kNegateA : 0u);
+      constexpr uint32_t kOuts = mma_shape(!kHalf, kTileRows, Sh::kPart, true);
       constexpr uint32_t kStageStep = Sh::kStageBytes / 16;  // in descriptors
       const uint32_t tm = same_in_all(tmem);
       const uint32_t s_at = tm + t * kKeys, p_at = tm + Sh::kP + t * Sh::kPStep;

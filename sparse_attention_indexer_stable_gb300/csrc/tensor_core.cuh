@@ -128,9 +128,9 @@ __device__ __forceinline__ uint64_t rows_across_k(uint32_t smem, uint32_t next) 
 }
 
 // fp32 sums of M x N products of two fp16 (or two bf16) operands.
-__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int m, int n, bool negate_a,
-                                                 bool b_across_k) {
-  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (negate_a ? 1u << 13 : 0u) |
+constexpr uint32_t kNegateA = 1u << 13;
+__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int m, int n, bool b_across_k) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) |
          (b_across_k ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 

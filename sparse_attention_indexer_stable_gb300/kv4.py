@@ -153,7 +153,9 @@ def kv4_extend(table, lens, counts, free, used, places, page_size, num_pages, ou
     that were missing.
     page_size and num_pages are those of the caches that the table serves.
     out: an earlier Kv4Step to write to; its lens may be `lens` and its used
-    `used`, which then advance in place.
+    `used`, which then advance in place.  Without it all seven are parts of one
+    allocation, which lives as long as any of them: keep a clone, or a copy in
+    tensors of your own, of what is to outlive the step.
     """
     r = (_bound or _bind()).extend(table, lens, counts, free, used, places, page_size, num_pages,
                                    out, _handle(stream))

@@ -34,9 +34,11 @@ class Rotary:
     `fast` times are kept, and between the two it is a linear blend.
     magnitude: multiplies the turned elements (default 1, with original
     0.1 ln(factor) + 1).
-    frequencies: radians a position for each pair, in place of all of these.
-    Made outside of a CUDA graph's capture: it copies the frequencies to the
-    device.
+    frequencies: radians a position for each pair, in place of all of these (for
+    checkpoints with another rule, such as a blend that is linear in the pair's
+    index instead of its turns).
+    Made once, outside of a CUDA graph's capture: exact fractions on the host, a
+    tenth of a millisecond or two, and a copy to the device.
     """
 
     __slots__ = ("dim", "interleaved", "magnitude", "frequencies", "turns", "device")
@@ -108,13 +110,20 @@ def prompt_attention(q, k, v, starts, causal=True, window=0, scale=None, softcap
     of q's dtype; query head h reads key/value head h // (q_heads // heads).  Any
     row and head strides; what is not 16-byte aligned, or whose strides are 0 or
     no multiples of 8 elements, is copied first.
+    Products and sums are fp32; probabilities are rounded to q's dtype before they
+    meet the values.  No gradients: inputs that require them are taken as they are.
     starts: int32 (sequences + 1,), ascending, as kv4_extend gives them: sequence
     b is rows starts[b] to starts[b + 1] - 1.  Row i of a sequence sees its rows
     j <= i (all of them with causal=False) and, with a window, j > i - window.
     scale: default (None or 0) D ** -0.5.  softcap: scores become
     softcap * tanh(score / softcap); 0: none.
-    Rows of no sequence are left as they are in out and lse; where these are
-    allocated here, such rows hold no particular value.
+    out, lse: contiguous; they share no memory with the inputs.  Rows of no sequence
+    are left as they are in them; where they are allocated here, such rows hold no
+    particular value.
+    Largest scores beyond 2^20 ln 2, and infinities or NaN among values just
+    behind what a row sees, are right but slow (some 200 times, for those rows).
+    Should a copy not land within about a second, the rows that wait for it are NaN
+    and dcp_topk_device_status() has DCP_DEVICE_COPY_TIMEOUT set.
     """
     r = (kv4._bound or kv4._bind()).prompt_attention(q, k, v, starts, causal, window, scale,
                                                      softcap, out, lse, _handle(stream))

@@ -93,7 +93,7 @@ dcp_status dcp_kv4_read(const dcp_kv4_cache* cache, void* k, void* v, int dtype,
  * the cache's values are exact in fp16) and summed in fp32; the probabilities
  * are rounded to fp16 for the second product only, their sum is kept in fp32
  * (compensated).  Scores beyond 1e8 in magnitude, where fp32's steps span most
- * of the exponent's range, may give NaN.
+ * of the exponent's range, may give NaN, or lose their weight without a sign.
  */
 typedef struct {
     const void* q;          /* [rows][q_heads][dim] of dtype (fp16 or bf16), dim contiguous */

@@ -27,8 +27,8 @@ extern "C" {
  * whole turns,
  *   y = magnitude * (x0 cos 2 pi a - x1 sin 2 pi a, x1 cos 2 pi a + x0 sin 2 pi a)
  * and the head's other elements are copied.  The product is taken modulo 2^64,
- * so the angle is exact to 2^-32 of a turn for every position; a negative
- * position turns back.  Products and sums are fp32, rounded once at the end.
+ * so the angle is exact to 2^-34 of a turn for every position, and to fp32's
+ * 2^-24 of itself from there; a negative position turns back.  Products and sums are fp32, rounded once at the end.
  */
 typedef struct {
     const void* q;          /* [tokens][q_heads][dim] of dtype, dim contiguous */

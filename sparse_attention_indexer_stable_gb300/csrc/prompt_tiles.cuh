@@ -16,10 +16,11 @@
 // - bf16, which has fp32's range: set at the maximum, until P passes 2^60.
 //
 // What bounds a step is the tensor cores' time for both products, or, for heads
-// of 64, the exponentials; the rest has to happen meanwhile:
+// of 64, the chain of a row's thread (wait, load, 128 exponentials, hand over; no
+// pipe is above 45%); the rest has to happen meanwhile:
 // - Two tiles to an SM: while one's rows are exponentiated, the tensor cores work
 //   on the other's.  Heads of 128: one CTA with both tiles, which share the keys
-//   (a CTA each: 3110 us for 16384 rows, instead of 2470).  Heads of 64: two CTAs
+//   (a CTA each: 26% longer for 16384 rows).  Heads of 64: two CTAs
 //   of a tile, whose ends do not coincide (one with both: 233 us, instead of 212,
 //   for 16 texts of 1200 rows).  Heads of 256 leave room for one tile.
 // - Heads of 128: S and O of two tiles fill tensor memory, P takes S's place.
@@ -31,9 +32,11 @@
 //   one a tile's products, so that the next unit's copies and first S overlap the
 //   last one's end.
 //
-// Measured: one prompt of 16384 rows, 64 heads of 128 over 8: 2749 us, 1.60 PFLOP/s,
-// 83% of the measured matrix rate; a step of both tiles takes 2500 to 3200 cycles,
-// its products 2048.
+// Measured: one prompt of 16384 rows, 64 heads of 128 over 8: ten calls in a row, at
+// 2070 MHz, 2435 us each, 1.81 PFLOP/s, 93% of the matrix rate measured so; for
+// seconds, under the power cap and at 1770 MHz, 2690 us, 1.64 PFLOP/s, 94% of the
+// rate measured so.  A step of both tiles takes 2500 to 3200 cycles, its products
+// 2048.
 //
 // Masked scores are -infinity and their P is 0, but 0 times an infinite or NaN
 // value is NaN: rows whose O is not finite although their sum is are looked at by
@@ -644,9 +647,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
     };
     int s_round = 0, o_round = 0;  // phases of s_full and o_done
     // When the CTA has given up the rest of the unit is computed on whatever there
-    // is, and becomes NaN.  A wait without its own limit, that ends because those
-    // of the other warps do, takes 2390 us where this one takes 2433 (16384 rows,
-    // 64 heads of 128), and 289 where this one takes 302 (33 x 2048, 12 of 64).
+    // is, and becomes NaN.  (Without a limit of their own, ending because those of
+    // the other warps do, these waits took 2% less for 16384 rows of 64 heads of 128,
+    // 4% less for 33 x 2048 of 12 of 64.)
     auto wait_here = [&](unsigned long long* bar, uint32_t parity) {
       wait_for(bar, parity, patience);
       __syncwarp();
@@ -716,9 +719,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
         // Caps and masks: in tensor memory, in a loop.  (Unrolled over the registers
         // they were so much code that instructions came from the second-level
         // cache: with caps 1977 us instead of 577, without 419 instead of 317, for 33
-        // prompts of 2048 rows with a window of 1000.  Caps by 32 scores: 546 us
-        // for prompts of 1 to 4097 rows, by 16 586; but 597 and 552 where one score in
-        // some hundred is beyond the cap.)
+        // prompts of 2048 rows with a window of 1000.  Caps by 32 scores: 466 us
+        // there where all are within the cap, 657 where many are beyond; by 16
+        // scores 516 and 704.)
         auto finish_scores = [&] {
           constexpr int kPiece = kCapped ? 32 : 16;
 #pragma unroll 1

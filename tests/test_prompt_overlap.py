@@ -6,17 +6,18 @@ import sparse_attention_indexer_stable_gb300 as dk
 from .test_prompt_capi import prompt
 
 # addresses that are never read: every call is refused.  3 rows of 4 query heads
-# and one key/value head of 128, 2 bytes each: q 3072 bytes, k and v 768, lse 48.
+# and one key/value head of 128, 2 bytes each
+Q, KV, LSE = 3 * 4 * 256, 3 * 256, 3 * 4 * 4
 APART = dict(q=0x10000, k=0x20000, v=0x30000, starts=0x40000, out=0x50000, lse=0x60000)
 
 
 @pytest.mark.parametrize("change", [
-    dict(out=0x10000), dict(out=0x10000 + 3072 - 16), dict(out=0x10000 - 3072 + 16),
-    dict(out=0x20000), dict(out=0x20000 + 768 - 16), dict(out=0x30000 - 3072 + 16),
-    dict(lse=0x10000 + 512), dict(lse=0x20000 - 4), dict(lse=0x30000 + 764),
-    dict(out=0x40000), dict(lse=0x40004), dict(lse=0x50000 + 3068), dict(lse=0x50000 - 44),
+    dict(out=0x10000), dict(out=0x10000 + Q - 16), dict(out=0x10000 - Q + 16),
+    dict(out=0x20000), dict(out=0x20000 + KV - 16), dict(out=0x30000 - Q + 16),
+    dict(lse=0x10000 + 512), dict(lse=0x20000 - 4), dict(lse=0x30000 + KV - 4),
+    dict(out=0x40000), dict(lse=0x40004), dict(lse=0x50000 + Q - 4), dict(lse=0x50000 - LSE + 4),
     # between the rows of a wider buffer, which it reaches at its end or its beginning
-    dict(q_row=4096, out=0x10000 + 8192 - 3072 + 16), dict(q_row=4096, lse=0x10000 + 8192 - 4),
+    dict(q_row=4096, out=0x10000 + 8192 - Q + 16), dict(q_row=4096, lse=0x10000 + 8192 - 4),
     # head after head: 3 rows of head 2
     dict(q_row=128, q_head=1024, lse=0x10000 + 2 * 2048 + 512 - 4),
 ])

@@ -134,7 +134,7 @@ def test_rows_behind_the_last_sequence_cost_nothing(dk, dim):  # noqa: F811
             b.record()
             torch.cuda.synchronize()
             one.append(a.elapsed_time(b))
-        times.append(sorted(one)[3])
+        times.append(min(one))
     assert times[1] + times[3] <= 1.1 * (times[0] + times[2])
 
 
